@@ -117,7 +117,7 @@ def prepare(case, seed):
     cap = (case["rows"] + 7) // 8 * 8
     lens = lengths(case, seed)
     state = {"case": case, "lens": torch.tensor(lens, dtype=torch.int32, device=DEV)}
-    names = ("k_codes", "k_params", "v_codes", "v_params")
+    names = ("k_codes", "k_words", "v_codes", "v_words")
     if case["op"] == "write":
         # caches that already hold something: random codes, scales near one
         state["cache"] = dict(zip(names, (
@@ -213,7 +213,7 @@ def plain_write(state):
         x = state[name] if taken is None else state[name][taken]
         codes, words = quantise(x[None])                     # [1, H, rows, ..]
         cache[name + "_codes"][b, :, row] = codes[0].transpose(0, 1)
-        cache[name + "_params"][b, :, row] = words[0].transpose(0, 1)
+        cache[name + "_words"][b, :, row] = words[0].transpose(0, 1)
     return plain_read(state)
 
 
@@ -221,7 +221,7 @@ def plain_read(state):
     cache = state["cache"]
     b, row, taken = places(state)
     for name, out in zip(("k", "v"), state["out"]):
-        x = values(cache[name + "_codes"][b, :, row], cache[name + "_params"][b, :, row])
+        x = values(cache[name + "_codes"][b, :, row], cache[name + "_words"][b, :, row])
         if taken is not None:
             x = torch.where(taken[..., None, None], x, out.float())
         out.copy_(x.to(torch.bfloat16))
@@ -232,8 +232,8 @@ def plain_attend(state):
     case, cache, q = state["case"], state["cache"], state["q"].float()
     B, Nq, H, d = q.shape
     Hkv, window = case["Hkv"], case["window"]
-    k = values(cache["k_codes"], cache["k_params"])
-    v = values(cache["v_codes"], cache["v_params"])
+    k = values(cache["k_codes"], cache["k_words"])
+    v = values(cache["v_codes"], cache["v_words"])
     rows = k.shape[2]
     q = q.view(B, Nq, Hkv, H // Hkv, d).permute(0, 2, 1, 3, 4).reshape(B, Hkv, -1, d)
     x = torch.matmul(q, k.transpose(-1, -2)) * (1 / math.sqrt(d))
@@ -326,7 +326,7 @@ def exact(case, seed):
             got = torch.zeros(case["B"], case["N"], case["Hkv"], case["d"], dtype=torch.float64, device=DEV)
             for b, (at, n) in enumerate(zip(state["starts"].tolist(), state["lens"].tolist())):
                 part = exact_cache_values(cache[name + "_codes"][b, :, at:at + n],
-                                          cache[name + "_params"][b, :, at:at + n])
+                                          cache[name + "_words"][b, :, at:at + n])
                 got[b, :n] = part.transpose(0, 1)
             outs.append(got)
         return tuple(outs)
@@ -343,8 +343,8 @@ def exact(case, seed):
         hidden = (key > at) | ((key <= at - window) if window else (key > at))
         seen = (~hidden).any(-1)
         for h in range(case["Hkv"]):
-            k = exact_cache_values(cache["k_codes"][b, h, :n], cache["k_params"][b, h, :n])
-            v = exact_cache_values(cache["v_codes"][b, h, :n], cache["v_params"][b, h, :n])
+            k = exact_cache_values(cache["k_codes"][b, h, :n], cache["k_words"][b, h, :n])
+            v = exact_cache_values(cache["v_codes"][b, h, :n], cache["v_words"][b, h, :n])
             for head in range(h * group, h * group + group):
                 x = (q[b, :, head] @ k.T / math.sqrt(d)).masked_fill(hidden, -math.inf)
                 lse[b, head] = torch.logsumexp(x, -1)
