@@ -137,7 +137,8 @@ def prepare(case, seed):
             state["cu"] = cu.to(DEV)
         return state
     full = (B, cap, Hkv, d)
-    state["cache"] = dict(zip(names, (*quantise(normal(full, g, 0.6)), *quantise(normal(full, g)))))
+    state["cache"] = dict(zip(names, (t.contiguous() for t in (*quantise(normal(full, g, 0.6)),
+                                                               *quantise(normal(full, g))))))
     if case["op"] == "read":
         shape = [B, case["N"], Hkv, d]
         state["starts"] = torch.randint(0, case["rows"] - case["N"] + 1, (B,), generator=g, device=DEV,
