@@ -183,6 +183,75 @@ int fa_fwd_kvcache_num_splits(int B, int H, int Nq, int Nk, int d);
 size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits);
 
 /*
+ * 4-bit key/value cache: a cache at a quarter of the bf16 one's bytes, the
+ * writing of new rows into it, reading rows back, and attention over it (the
+ * inference interface with cached keys and values, FlashAttention encyclopedia
+ * page, "software integration", with a smaller cache; NOT exact attention over
+ * the keys and values that went in, exact attention over what they were
+ * rounded to).
+ *
+ * Format.  One row is one token of one key/value head, x of d channels (d 64
+ * or 128).  With hi = max(0, max x) and lo = min(0, min x):
+ *     s = the smallest number of 4 significant bits with 15 s >= hi - lo,
+ *         and at least 2^-126,
+ *     z = floor(-lo / s + 1/2),     c = min(15, floor(x / s + 1/2) + z),
+ * and the row stands for s (c - z): at most s / 2 from x, and a bf16 number
+ * (infinity past bf16's range, which rows with an element of 2^126 or more can
+ * reach).  A row that holds NaN or infinity stands for NaN in every channel.
+ *   codes : uint8 [B, Hkv, Nk, d / 2], channel 2j in the low and 2j + 1 in the
+ *           high half of byte j.
+ *   words : 16-bit [B, Hkv, Nk], the bf16 pattern of s with z in its low four
+ *           bits (which are zero in s).
+ * K and V have one array of each, 16-byte aligned.  Nk, the rows a sequence
+ * has room for, is a multiple of 8 (FA_ERR_BAD_SHAPE otherwise).
+ *
+ * fa_quantize_kv4 writes bf16 rows k, v into the cache; fa_dequantize_kv4
+ * writes cache rows to k, v as bf16, without any rounding.  Row i of sequence
+ * b stands at cache row starts[b] + i (starts: device int32 [B], NULL for all
+ * 0), for 0 <= i < n_b:
+ *   fixed length : k, v [B, N, Hkv, d]; n_b = lens[b] (device int32 [B],
+ *           clamped to [0, N]), or N when lens is NULL.
+ *   packed : k, v [N, Hkv, d] with cu_seqlens (device int32 [B + 1], at most
+ *           2048 sequences), n_b = cu_seqlens[b + 1] - cu_seqlens[b]; lens
+ *           must be NULL.
+ * Rows at or past n_b, rows of a packed buffer outside every sequence, and
+ * rows whose cache row is below 0 or not below Nk are neither read nor
+ * written on either side.  Two rows of one call never share a cache row; calls
+ * that write the same rows are the caller's to order.
+ *
+ * fa_fwd_kv4: attention of q against the cache, arguments as fa_fwd_kvcache
+ * with these differences.  H query heads read Hkv key/value heads, H a
+ * multiple of Hkv: query head h reads head h / (H / Hkv).  Sequence b uses
+ * cache rows 0 .. nk_b - 1 (seqlens_k, clamped to [0, Nk]; NULL for Nk), the
+ * queries are the last Nq of those positions, and rows past nk_b are never
+ * used.  Queries without a key get O = 0, LSE = -inf.  A row whose K or V
+ * stands for NaN makes O NaN (and LSE unspecified) for the queries that see
+ * it, and reaches no others.
+ *   Up to 32 query rows to a key/value head (Nq * H / Hkv) run on a kernel
+ * that multiplies the 4-bit codes as they are; more are run by reading the
+ * rows in use back into the workspace for the tensor-core forward.
+ *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, splits) bytes,
+ * 16-byte aligned (0, then NULL is allowed, for few rows and one split);
+ * contents on entry do not matter.  Calls that may overlap on the GPU need
+ * one each.  num_splits as fa_fwd_kvcache, 0 for fa_fwd_kv4_num_splits's
+ * choice.
+ * Errors as fa_fwd_kvcache; H not a multiple of Hkv is FA_ERR_BAD_SHAPE.
+ */
+int fa_quantize_kv4(const void* k, const void* v, void* k_codes, void* k_words, void* v_codes,
+                    void* v_words, int B, int N, int Hkv, int Nk, int d, const int* cu_seqlens,
+                    const int* starts, const int* lens, cudaStream_t stream);
+int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_codes,
+                      const void* v_words, void* k, void* v, int B, int N, int Hkv, int Nk, int d,
+                      const int* cu_seqlens, const int* starts, const int* lens,
+                      cudaStream_t stream);
+int fa_fwd_kv4_num_splits(int B, int H, int Hkv, int Nq, int Nk, int d);
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits);
+int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
+               const void* v_words, void* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
+               float scale, int causal, int window, const int* seqlens_k, int num_splits,
+               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * FP8 forward (block-quantised e4m3; NOT exact attention -- a separate,
  * lower-precision path).  The FlashAttention encyclopedia page (FlashAttention-3
  * paragraph) names an FP8 path with block quantisation and a processing step
@@ -321,8 +390,8 @@ int fa_get_device_error(cudaStream_t stream);
  * (up to 1024 launches per kernel kind; later ones are not recorded).
  * fa_profile_end() waits for the recorded events, stops recording, and writes
  * for each kind k (0 forward, 1 D pre-pass, 2 dK/dV, 3 dQ, 4 decode, 5 decode
- * split merge, 6 FP8 quantisation, 7 FP8 forward, 8 single-kernel backward,
- * 9 its dQ conversion) the summed device
+ * split merge, 6 quantisation (FP8; 4-bit cache rows written or read back),
+ * 7 FP8 forward, 8 single-kernel backward, 9 its dQ conversion) the summed device
  * milliseconds ms[k] and the number of recorded launches counts[k] (arrays of
  * FA_PROFILE_KINDS entries).
  * Either output pointer may be NULL.  The events are created once per device

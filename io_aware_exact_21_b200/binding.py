@@ -33,6 +33,14 @@ SIGNATURES = {
     "fa_fp8_vt_bytes": (_SZ, [_I, _I, _I, _I]),
     "fa_quantize_fp8": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP]),
     "fa_fwd_fp8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _I, _VP]),
+    "fa_quantize_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP,
+                             _VP]),
+    "fa_dequantize_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP,
+                               _VP]),
+    "fa_fwd_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP,
+                        _I, _VP, _SZ, _VP]),
+    "fa_fwd_kv4_num_splits": (_I, [_I, _I, _I, _I, _I, _I]),
+    "fa_fwd_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _I,
                     _VP, _VP, _SZ, _VP]),
@@ -142,6 +150,41 @@ def fa_fwd_kvcache_num_splits(B, H, Nq, Nk, d) -> int:
 def fa_fwd_kvcache_workspace_size(B, H, Nq, d, num_splits) -> int:
     return int(load_library().fa_fwd_kvcache_workspace_size(int(B), int(H), int(Nq), int(d),
                                                             int(num_splits)))
+
+
+def fa_quantize_kv4(k, v, k_codes, k_words, v_codes, v_words, B, N, Hkv, Nk, d, cu_seqlens, starts,
+                    lens, stream=None) -> int:
+    return load_library().fa_quantize_kv4(_ptr(k), _ptr(v), _ptr(k_codes), _ptr(k_words),
+                                          _ptr(v_codes), _ptr(v_words), int(B), int(N), int(Hkv),
+                                          int(Nk), int(d), _ptr(cu_seqlens), _ptr(starts),
+                                          _ptr(lens), _stream(stream))
+
+
+def fa_dequantize_kv4(k_codes, k_words, v_codes, v_words, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts,
+                      lens, stream=None) -> int:
+    return load_library().fa_dequantize_kv4(_ptr(k_codes), _ptr(k_words), _ptr(v_codes),
+                                            _ptr(v_words), _ptr(k), _ptr(v), int(B), int(N),
+                                            int(Hkv), int(Nk), int(d), _ptr(cu_seqlens),
+                                            _ptr(starts), _ptr(lens), _stream(stream))
+
+
+def fa_fwd_kv4(q, k_codes, k_words, v_codes, v_words, o, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
+               window, seqlens_k, num_splits, workspace, workspace_bytes, stream=None) -> int:
+    return load_library().fa_fwd_kv4(_ptr(q), _ptr(k_codes), _ptr(k_words), _ptr(v_codes),
+                                     _ptr(v_words), _ptr(o), _ptr(lse), int(B), int(H), int(Hkv),
+                                     int(Nq), int(Nk), int(d), float(scale), int(causal),
+                                     int(window), _ptr(seqlens_k), int(num_splits),
+                                     _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_fwd_kv4_num_splits(B, H, Hkv, Nq, Nk, d) -> int:
+    return int(load_library().fa_fwd_kv4_num_splits(int(B), int(H), int(Hkv), int(Nq), int(Nk),
+                                                    int(d)))
+
+
+def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits) -> int:
+    return int(load_library().fa_fwd_kv4_workspace_size(int(B), int(H), int(Hkv), int(Nq), int(Nk),
+                                                        int(d), int(num_splits)))
 
 
 def fa_fp8_vt_bytes(B, H, N, d) -> int:
@@ -387,6 +430,143 @@ def forward_kvcache(q, k_cache, v_cache, seqlens_k=None, causal=False, window=0,
                           seqlens_k, ns, workspace,
                           0 if workspace is None else workspace.numel(), stream),
            "fa_fwd_kvcache")
+    return out, lse
+
+
+KV4_NAMES = ("k_codes", "k_words", "v_codes", "v_words")
+
+
+def kv4_cache(B, rows, Hkv, d, device="cuda"):
+    """An empty 4-bit key/value cache with room for ``rows`` tokens (rounded up
+    to a multiple of 8) of B sequences and Hkv heads of d channels: a dict of
+    k_codes, v_codes (uint8 [B, Hkv, Nk, d / 2]) and k_words, v_words (int16
+    [B, Hkv, Nk]).  Zeros: every row reads as 0."""
+    import torch
+    if d not in (64, 128):
+        raise ValueError("d must be 64 or 128")
+    if B < 0 or rows < 0 or Hkv <= 0:
+        raise ValueError("B and rows must not be negative, Hkv must be positive")
+    Nk = (rows + 7) // 8 * 8
+    return {n: torch.zeros((B, Hkv, Nk, d // 2), dtype=torch.uint8, device=device)
+            if n.endswith("codes") else
+            torch.zeros((B, Hkv, Nk), dtype=torch.int16, device=device) for n in KV4_NAMES}
+
+
+def _kv4_shape(cache, device):
+    """(B, Hkv, Nk, d) of a 4-bit cache, its tensors checked against each other."""
+    import torch
+    for n in KV4_NAMES:
+        if cache.get(n) is None:
+            raise ValueError("cache[%r] is required" % n)
+    _rank(cache["k_codes"], "k_codes", (4,))
+    B, Hkv, Nk, half = cache["k_codes"].shape
+    for n in KV4_NAMES:
+        if n.endswith("codes"):
+            _expect(cache[n], n, (B, Hkv, Nk, half), torch.uint8, device)
+        else:
+            _expect(cache[n], n, (B, Hkv, Nk), torch.int16, device)
+    return B, Hkv, Nk, 2 * half
+
+
+def _kv4_rows(t, B, Hkv, d, cu_seqlens, starts, lens):
+    """Checks the rows' side of a write or read; returns its N argument."""
+    import torch
+    dev = t.device
+    if cu_seqlens is None:
+        _rank(t, "k", (4,))
+        N = t.shape[1]
+        shape = (B, N, Hkv, d)
+    else:
+        if lens is not None:
+            raise ValueError("lens and cu_seqlens exclude each other")
+        _rank(t, "k (packed)", (3,))
+        N = t.shape[0]
+        shape = (N, Hkv, d)
+        _expect(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    for x, name in ((starts, "starts"), (lens, "lens")):
+        if x is not None:
+            _expect(x, name, (B,), torch.int32, dev)
+    return N, shape
+
+
+def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=None):
+    """Write new key/value rows into a 4-bit cache (``kv4_cache``): bf16 k, v
+    [B, N, Hkv, d], row i of sequence b at cache row ``starts[b] + i`` (int32
+    CUDA tensor, None for 0), the first ``lens[b]`` rows of each (None for
+    all); or packed [T, Hkv, d] with int32 ``cu_seqlens``.  Rows that fall
+    outside the cache are left out.  Returns the cache."""
+    import torch
+    _rank(k, "k", (3, 4))
+    B, Hkv, Nk, d = _kv4_shape(cache, k.device)
+    N, shape = _kv4_rows(k, B, Hkv, d, cu_seqlens, starts, lens)
+    for t, name in ((k, "k"), (v, "v")):
+        _expect(t, name, shape, torch.bfloat16, k.device)
+    _check(fa_quantize_kv4(k, v, *(cache[n] for n in KV4_NAMES), B, N, Hkv, Nk, d, cu_seqlens, starts,
+                           lens, stream), "fa_quantize_kv4")
+    return cache
+
+
+def dequantize_kv4(cache, rows=None, starts=None, lens=None, cu_seqlens=None, out=None, stream=None):
+    """Read rows of a 4-bit cache back as bf16 (k, v) [B, rows, Hkv, d]
+    (``rows``: the cache's room when not given), or packed [rows, Hkv, d] with
+    ``cu_seqlens``; starts and lens as quantize_kv4.  Rows that belong to no
+    sequence or fall outside the cache keep what ``out`` holds (zeros when it
+    is not given)."""
+    import torch
+    dev = cache["k_codes"].device
+    B, Hkv, Nk, d = _kv4_shape(cache, dev)
+    if out is None:
+        if rows is None and cu_seqlens is not None:
+            raise ValueError("a packed read needs rows or out")
+        n = Nk if rows is None else rows
+        shape = (B, n, Hkv, d) if cu_seqlens is None else (n, Hkv, d)
+        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    k, v = out
+    N, shape = _kv4_rows(k, B, Hkv, d, cu_seqlens, starts, lens)
+    if rows is not None and rows != N:
+        raise ValueError("out holds %d rows, rows is %d" % (N, rows))
+    for t, name in ((k, "k"), (v, "v")):
+        _expect(t, name, shape, torch.bfloat16, dev)
+    _check(fa_dequantize_kv4(*(cache[n] for n in KV4_NAMES), k, v, B, N, Hkv, Nk, d, cu_seqlens,
+                             starts, lens, stream), "fa_dequantize_kv4")
+    return k, v
+
+
+def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, num_splits=0, out=None,
+                lse=None, workspace=None, stream=None):
+    """Attention against a 4-bit cache: q [B, Nq, H, d] bf16, H a multiple of
+    the cache's Hkv (query head h reads head h // (H // Hkv)); sequence b uses
+    its first seqlens_k[b] rows (int32 CUDA tensor, or None for all), queries
+    are the last Nq of those positions.  Returns (O, LSE)."""
+    import torch
+    _rank(q, "q", (4,))
+    B, Nq, H, d = q.shape
+    dev = q.device
+    _expect(q, "q", q.shape, torch.bfloat16, dev)
+    cB, Hkv, Nk, cd = _kv4_shape(cache, dev)
+    if (cB, cd) != (B, d):
+        raise ValueError("the cache holds %d sequences of d = %d, q has %d of %d" % (cB, cd, B, d))
+    if Hkv == 0 or H % Hkv:
+        raise ValueError("q has %d heads, not a multiple of the cache's %d" % (H, Hkv))
+    if seqlens_k is not None:
+        _expect(seqlens_k, "seqlens_k", (B,), torch.int32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    _expect(out, "out", q.shape, torch.bfloat16, dev)
+    _expect(lse, "lse", (B, H, Nq), torch.float32, dev)
+    ns = num_splits if num_splits > 0 else fa_fwd_kv4_num_splits(B, H, Hkv, Nq, Nk, d)
+    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, ns)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _expect_bytes(workspace, "workspace", need, dev)
+    _check(fa_fwd_kv4(q, *(cache[n] for n in KV4_NAMES), out, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
+                      window, seqlens_k, ns, workspace, 0 if workspace is None else workspace.numel(),
+                      stream), "fa_fwd_kv4")
     return out, lse
 
 

@@ -14,6 +14,8 @@
 #include "decode_kernel.cuh"
 #include "fp8_quant.cuh"
 #include "fwd_kernel.cuh"
+#include "kv4_decode.cuh"
+#include "kv4_rows.cuh"
 
 namespace {
 
@@ -101,6 +103,19 @@ cudaError_t decode_set_smem_limits() {
     return e == cudaSuccess ? decode_set_smem_limits_d<128>() : e;
 }
 
+template <int D, int NT>
+cudaError_t kv4_set_smem_limit() {
+    return allow_smem(fa::kv4_decode_kernel<D, NT>, fa::Kv4DecCfg<D, NT>::SMEM);
+}
+
+cudaError_t kv4_set_smem_limits() {
+    cudaError_t e = kv4_set_smem_limit<64, 1>();
+    if (e == cudaSuccess) e = kv4_set_smem_limit<64, 2>();
+    if (e == cudaSuccess) e = kv4_set_smem_limit<128, 1>();
+    if (e == cudaSuccess) e = kv4_set_smem_limit<128, 2>();
+    return e;
+}
+
 // Per-device one-time set-up: SM count, the device address of the error word,
 // the driver's tensor-map encoder and the kernels' shared-memory limits.
 int device_setup(DeviceState** out) {
@@ -126,7 +141,7 @@ int device_setup(DeviceState** out) {
         }
         if (allow_smem(fa::fwd_kernel<64>, fa::FwdCfg<64>::SMEM_BYTES) != cudaSuccess ||
             allow_smem(fa::fwd_kernel<128>, fa::FwdCfg<128>::SMEM_BYTES) != cudaSuccess ||
-            decode_set_smem_limits() != cudaSuccess ||
+            decode_set_smem_limits() != cudaSuccess || kv4_set_smem_limits() != cudaSuccess ||
             allow_smem(fa::fwd_kernel<128, true>, fa::FwdCfg<128, true>::SMEM_BYTES) != cudaSuccess ||
             allow_smem(fa::fwd_kernel<64, false, true>, fa::FwdCfg<64>::SMEM_BYTES) != cudaSuccess ||
             allow_smem(fa::fwd_kernel<128, false, true>, fa::FwdCfg<128>::SMEM_BYTES) != cudaSuccess ||
@@ -318,6 +333,31 @@ size_t decode_workspace_bytes(int B, int H, int Nq, int d, int ns) {
     return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
+// The merge of a split decode.  Programmatic dependent launch: its CTAs are
+// scheduled while the split kernel's last wave runs and wait on the device for it.
+template <int D>
+int launch_combine(float* o_part, float* lse_part, __nv_bfloat16* o, float* lse, int B, int H, int Nq,
+                   int nsplit, cudaStream_t stream) {
+    const int64_t warps = static_cast<int64_t>(B) * Nq * H;
+    const int blocks = static_cast<int>((warps + 7) / 8);
+    const int slot = prof_start(5, stream);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::combine_kernel<D>, static_cast<const float*>(o_part),
+                                             static_cast<const float*>(lse_part), o, lse, B * Nq, H, Nq,
+                                             nsplit);
+    prof_stop(5, slot, stream);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 template <int D>
 int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const fa::DecodeParams& p,
                   cudaStream_t stream) {
@@ -336,28 +376,212 @@ int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode
         fa::decode_kernel<D, 16><<<grid, T, S, stream>>>(mk, mv, p);
     prof_stop(4, slot, stream);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    if (p.nsplit > 1) {
-        const int64_t warps = static_cast<int64_t>(p.B) * p.Nq * p.H;
-        const int blocks = static_cast<int>((warps + 7) / 8);
-        const int slot2 = prof_start(5, stream);
-        // programmatic dependent launch: the merge's CTAs are scheduled while
-        // the split kernel's last wave runs and wait on the device for it
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(blocks);
-        cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = 0;
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::combine_kernel<D>, p.o_part, p.lse_part, p.o,
-                                                 p.lse, p.B * p.Nq, p.H, p.Nq, p.nsplit);
-        prof_stop(5, slot2, stream);
-        if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    return p.nsplit > 1 ? launch_combine<D>(p.o_part, p.lse_part, p.o, p.lse, p.B, p.H, p.Nq, p.nsplit, stream)
+                        : FA_OK;
+}
+
+// A chunk of queries against a padded bf16 cache with H / group heads: the
+// tensor-core forward, split along the keys when ns > 1 (partials in `part`).
+int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, int B, int H,
+                 int group, int Nq, int Nk, int d, float scale, int causal, int window,
+                 const int* seqlens_k, int ns, float* part, const DeviceState* st, cudaStream_t stream) {
+    const int64_t rows_q = static_cast<int64_t>(B) * Nq;
+    const int64_t rows_k = static_cast<int64_t>(B) * Nk;
+    const int Hk = H / group;
+    if (rows_q > (int64_t{1} << 31) - 1) return FA_ERR_BAD_SHAPE;
+    // with no cache rows at all the maps are pointed at q: every key tile is
+    // then read at rows [-128, 0), outside the map, so nothing of q is read
+    const void* kk = rows_k > 0 ? k_cache : q;
+    const void* vv = rows_k > 0 ? v_cache : q;
+    const int map_rows_k = rows_k > 0 ? Nk : Nq;
+    if (static_cast<int64_t>(map_rows_k) * Hk * d * 2 >= (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
+    CUtensorMap mq, mk, mv;
+    if (make_map(&mq, q, rows_q, H, d, 128) || make_map_cache(&mk, kk, B, map_rows_k, Hk, d, 128) ||
+        make_map_cache(&mv, vv, B, map_rows_k, Hk, d, 128))
+        return FA_ERR_CUDA;
+    fa::FwdParams p;
+    p.g.B = B;
+    p.g.H = H;
+    p.g.N = Nq;
+    p.g.T = static_cast<int>(rows_q);
+    p.g.cu_seqlens = nullptr;
+    p.g.causal = causal ? 1 : 0;
+    p.g.window = window > 0 ? window : 0;
+    p.g.Nk = Nk;
+    p.g.Tk = static_cast<int>(rows_k);
+    p.g.cu_seqlens_k = nullptr;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.error_word = st->error_word;
+    p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
+    p.fault_skip_v = 0;
+    p.nsplit = ns;
+    p.kv.seqused_k = seqlens_k;
+    p.kv.o_part = ns > 1 ? part : nullptr;
+    p.kv.lse_part = ns > 1 ? part + static_cast<size_t>(ns) * rows_q * H * d : nullptr;
+    p.kv.group = group;
+    int grid = st->num_sms;
+    const int64_t items = static_cast<int64_t>(B) * H * ns * ((Nq + 255) / 256);
+    if (items < grid) grid = static_cast<int>(items);
+    const int slot = prof_start(0, stream);
+    const int rc = d == 64 ? launch_fwd_cache<64>(mq, mk, mv, p, grid, stream)
+                           : launch_fwd_cache<128>(mq, mk, mv, p, grid, stream);
+    prof_stop(0, slot, stream);
+    if (rc != FA_OK || ns == 1) return rc;
+    const int64_t warps = rows_q * H;
+    const int slot2 = prof_start(5, stream);
+    if (d == 64)
+        fa::combine_kernel<64><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
+            p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
+    else
+        fa::combine_kernel<128><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
+            p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
+    prof_stop(5, slot2, stream);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// ------------------------------------------------------ 4-bit K/V cache --
+constexpr int kKv4DirectRows = 32;
+
+// Whether attention over the 4-bit cache runs on kv4_decode_kernel (query rows
+// to a key/value head: Nq * group) or reads the cache back for the forward.
+bool kv4_direct(int Nq, int group, int Nk) {
+    return static_cast<int64_t>(Nq) * group <= kKv4DirectRows || Nk == 0;
+}
+
+// Query rows a CTA of kv4_decode_kernel holds: 8 or 16.
+int kv4_block_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+int64_t kv4_row_blocks(int64_t rows) {
+    const int per = kv4_block_rows(rows);
+    return (rows + per - 1) / per;
+}
+
+// Split count of kv4_decode_kernel: as decode_splits, for its CTAs an SM and
+// at least 256 keys a split.
+int kv4_splits(int B, int H, int Hkv, int Nq, int Nk, int num_sms) {
+    const int group = H / Hkv;
+    if (!kv4_direct(Nq, group, Nk)) return prefill_splits(B, H, Nq, Nk, num_sms);
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
+    const int max_ns = std::max(1, std::min(fa::kDecMaxSplits, (Nk + 255) / 256));
+    const int64_t slots = (kv4_block_rows(rows) == 8 ? 2 : 3) * static_cast<int64_t>(num_sms);
+    int best = 1;
+    double best_fill = -1.0;
+    for (int ns = 1; ns <= max_ns; ++ns) {
+        const int64_t ctas = items * ns;
+        const int64_t waves = (ctas + slots - 1) / slots;
+        const double fill = static_cast<double>(ctas) / static_cast<double>(waves * slots);
+        if (fill >= 0.9) return ns;
+        if (fill > best_fill + 1e-9) {
+            best_fill = fill;
+            best = ns;
+        }
     }
-    return FA_OK;
+    return best;
+}
+
+// Bytes of the bf16 K (and of the V) that a chunk is read back into.
+size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
+    const size_t bytes = static_cast<size_t>(B) * Nk * Hkv * d * 2;
+    return (bytes + 255) & ~static_cast<size_t>(255);
+}
+
+size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int ns) {
+    const size_t part = decode_workspace_bytes(B, H, Nq, d, ns);
+    return kv4_direct(Nq, H / Hkv, Nk) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
+}
+
+bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
+    return B < 0 || Hkv <= 0 || Nk < 0 || Nk % 8 != 0 ||
+           static_cast<int64_t>(B) * Nk > (int64_t{1} << 31) - 1 ||
+           static_cast<int64_t>(B) * Nk * Hkv * d > (int64_t{1} << 40);
+}
+
+// Writes (kWrite) or reads the rows of p.place, K and V in one launch.
+template <int D, bool kWrite>
+int launch_kv4_rows(const fa::Kv4Params& p, int num_sms, cudaStream_t stream) {
+    const int64_t H = p.place.H;
+    // Eight steps a warp keep enough bytes in flight to stream; with too few
+    // rows for that, one step a warp spreads them over the SMs.
+    constexpr int TOK8 = fa::kv4_tokens<D, 8>(), TOK1 = fa::kv4_tokens<D, 1>();
+    const bool many = (p.rows + TOK8 - 1) / TOK8 * H >= static_cast<int64_t>(num_sms) * fa::kKv4Warps;
+    const int64_t tok = many ? TOK8 : TOK1;
+    const int64_t units = (p.rows + tok - 1) / tok * H;
+    if (units > (int64_t{1} << 31) - 1) return FA_ERR_BAD_SHAPE;
+    const dim3 grid(static_cast<unsigned>((units + fa::kKv4Warps - 1) / fa::kKv4Warps), 2);
+    const int slot = prof_start(6, stream);
+    constexpr int T = fa::kKv4Warps * 32;
+    if (kWrite) {
+        if (many) fa::kv4_write_kernel<D, 8><<<grid, T, 0, stream>>>(p);
+        else fa::kv4_write_kernel<D, 1><<<grid, T, 0, stream>>>(p);
+    } else {
+        if (many) fa::kv4_read_kernel<D, 8><<<grid, T, 0, stream>>>(p);
+        else fa::kv4_read_kernel<D, 1><<<grid, T, 0, stream>>>(p);
+    }
+    prof_stop(6, slot, stream);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// The checks and the launch that fa_quantize_kv4 and fa_dequantize_kv4 share.
+template <bool kWrite>
+int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_words, const void* v_codes,
+             const void* v_words, int B, int N, int Hkv, int Nk, int d, const int* cu_seqlens,
+             const int* starts, const int* lens, cudaStream_t stream) {
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
+    if (N < 0 || kv4_bad_cache(B, Hkv, Nk, d)) return FA_ERR_BAD_SHAPE;
+    if (cu_seqlens && (lens || B > fa::kMaxVarlenSeqs)) return FA_ERR_BAD_SHAPE;
+    const int64_t rows = cu_seqlens ? static_cast<int64_t>(N) : static_cast<int64_t>(B) * N;
+    if (rows > (int64_t{1} << 31) - 1 || rows * Hkv * d > (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
+    const int64_t rows_k = static_cast<int64_t>(B) * Nk;
+    if (rows > 0 && (!k || !v)) return FA_ERR_NULLPTR;
+    if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
+    if (misaligned(k) || misaligned(v) || misaligned(k_codes) || misaligned(v_codes) ||
+        misaligned(k_words) || misaligned(v_words) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(starts) & 3u) || (reinterpret_cast<uintptr_t>(lens) & 3u))
+        return FA_ERR_MISALIGNED;
+    if (rows == 0 || rows_k == 0) return FA_OK;
+    DeviceState* st = nullptr;
+    const int rc = device_setup(&st);
+    if (rc != FA_OK) return rc;
+    fa::Kv4Params p = {};
+    p.place.cu_seqlens = cu_seqlens;
+    p.place.starts = starts;
+    p.place.lens = lens;
+    p.place.B = B;
+    p.place.N = N;
+    p.place.H = Hkv;
+    p.place.Nk = Nk;
+    p.rows = rows;
+    p.x[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(k));
+    p.x[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+    p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+    p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+    p.words[0] = static_cast<uint16_t*>(const_cast<void*>(k_words));
+    p.words[1] = static_cast<uint16_t*>(const_cast<void*>(v_words));
+    return d == 64 ? launch_kv4_rows<64, kWrite>(p, st->num_sms, stream)
+                   : launch_kv4_rows<128, kWrite>(p, st->num_sms, stream);
+}
+
+template <int D, int NT>
+cudaError_t launch_kv4_decode_nt(const fa::Kv4DecodeParams& p, int grid, cudaStream_t stream) {
+    using C = fa::Kv4DecCfg<D, NT>;
+    fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+int launch_kv4_decode(const fa::Kv4DecodeParams& p, cudaStream_t stream) {
+    const int grid = p.B * p.Hkv * p.nsplit * p.row_blocks;
+    const int slot = prof_start(4, stream);
+    const cudaError_t e = kv4_block_rows(static_cast<int64_t>(p.Nq) * p.G) == 8
+                              ? launch_kv4_decode_nt<D, 1>(p, grid, stream)
+                              : launch_kv4_decode_nt<D, 2>(p, grid, stream);
+    prof_stop(4, slot, stream);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    return p.nsplit > 1 ? launch_combine<D>(p.o_part, p.lse_part, p.o, p.lse, p.B, p.H, p.Nq, p.nsplit, stream)
+                        : FA_OK;
 }
 
 // ------------------------------------------------ allocation-free backward --
@@ -448,6 +672,7 @@ int fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float* lse, 
         p.kv.seqused_k = nullptr;
         p.kv.o_part = nullptr;
         p.kv.lse_part = nullptr;
+        p.kv.group = 1;
         int grid = st->num_sms;
         const int64_t items = static_cast<int64_t>(B) * H * ((Nq + 255) / 256);
         if (items < grid) grid = static_cast<int>(items);
@@ -547,57 +772,8 @@ int fa_fwd_kvcache(const void* q, const void* k_cache, const void* v_cache, void
     if ((rc = check_ws(ns)) != FA_OK) return rc;
     if (Nq > fa::kDecMaxQ) {
         // a prefill chunk: the tensor-core forward, split along the keys when ns > 1
-        if (rows_q > (int64_t{1} << 31) - 1) return FA_ERR_BAD_SHAPE;
-        // with no cache rows at all the maps are pointed at q: every key tile is
-        // then read at rows [-128, 0), outside the map, so nothing of q is read
-        const void* kk = rows_k > 0 ? k_cache : q;
-        const void* vv = rows_k > 0 ? v_cache : q;
-        const int map_rows_k = rows_k > 0 ? Nk : Nq;
-        if (static_cast<int64_t>(map_rows_k) * H * d * 2 >= (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
-        CUtensorMap mq, mk, mv;
-        if (make_map(&mq, q, rows_q, H, d, 128) || make_map_cache(&mk, kk, B, map_rows_k, H, d, 128) ||
-            make_map_cache(&mv, vv, B, map_rows_k, H, d, 128))
-            return FA_ERR_CUDA;
-        fa::FwdParams p;
-        p.g.B = B;
-        p.g.H = H;
-        p.g.N = Nq;
-        p.g.T = static_cast<int>(rows_q);
-        p.g.cu_seqlens = nullptr;
-        p.g.causal = causal ? 1 : 0;
-        p.g.window = window > 0 ? window : 0;
-        p.g.Nk = Nk;
-        p.g.Tk = static_cast<int>(rows_k);
-        p.g.cu_seqlens_k = nullptr;
-        p.o = static_cast<__nv_bfloat16*>(o);
-        p.lse = lse;
-        p.scale_log2 = scale * 1.4426950408889634f;
-        p.error_word = st->error_word;
-        p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
-        p.fault_skip_v = 0;
-        p.nsplit = ns;
-        p.kv.seqused_k = seqlens_k;
-        p.kv.o_part = ns > 1 ? static_cast<float*>(workspace) : nullptr;
-        p.kv.lse_part = ns > 1 ? static_cast<float*>(workspace) + static_cast<size_t>(ns) * rows_q * H * d
-                               : nullptr;
-        int grid = st->num_sms;
-        const int64_t items = static_cast<int64_t>(B) * H * ns * ((Nq + 255) / 256);
-        if (items < grid) grid = static_cast<int>(items);
-        const int slot = prof_start(0, stream);
-        rc = d == 64 ? launch_fwd_cache<64>(mq, mk, mv, p, grid, stream)
-                     : launch_fwd_cache<128>(mq, mk, mv, p, grid, stream);
-        prof_stop(0, slot, stream);
-        if (rc != FA_OK || ns == 1) return rc;
-        const int64_t warps = rows_q * H;
-        const int slot2 = prof_start(5, stream);
-        if (d == 64)
-            fa::combine_kernel<64><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
-                p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
-        else
-            fa::combine_kernel<128><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
-                p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
-        prof_stop(5, slot2, stream);
-        return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+        return launch_chunk(q, k_cache, v_cache, o, lse, B, H, 1, Nq, Nk, d, scale, causal, window,
+                            seqlens_k, ns, static_cast<float*>(workspace), st, stream);
     }
     // With no cache rows every split is empty and no tile is loaded; the maps
     // still need a valid base, so they are pointed at q.
@@ -628,6 +804,126 @@ int fa_fwd_kvcache(const void* q, const void* k_cache, const void* v_cache, void
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
     p.fault_skip = g_fault_mode == 2 ? 1 : 0;
     return d == 64 ? launch_decode<64>(mk, mv, p, stream) : launch_decode<128>(mk, mv, p, stream);
+}
+
+int fa_quantize_kv4(const void* k, const void* v, void* k_codes, void* k_words, void* v_codes,
+                    void* v_words, int B, int N, int Hkv, int Nk, int d, const int* cu_seqlens,
+                    const int* starts, const int* lens, cudaStream_t stream) {
+    return kv4_rows<true>(k, v, k_codes, k_words, v_codes, v_words, B, N, Hkv, Nk, d, cu_seqlens, starts,
+                          lens, stream);
+}
+
+int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_codes,
+                      const void* v_words, void* k, void* v, int B, int N, int Hkv, int Nk, int d,
+                      const int* cu_seqlens, const int* starts, const int* lens, cudaStream_t stream) {
+    return kv4_rows<false>(k, v, k_codes, k_words, v_codes, v_words, B, N, Hkv, Nk, d, cu_seqlens, starts,
+                           lens, stream);
+}
+
+int fa_fwd_kv4_num_splits(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    (void)d;
+    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nk <= 0 || Nq <= 0) return 1;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms <= 0) sms = 148;
+    return kv4_splits(B, H, Hkv, Nq, Nk, sms);
+}
+
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits) {
+    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
+    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, num_splits);
+}
+
+int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
+               const void* v_words, void* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
+               float scale, int causal, int window, const int* seqlens_k, int num_splits,
+               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!q || !o || !lse) return FA_ERR_NULLPTR;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
+    if (H <= 0 || Nq < 0 || kv4_bad_cache(B, Hkv, Nk, d) || H % Hkv != 0) return FA_ERR_BAD_SHAPE;
+    if (num_splits < 0 || num_splits > fa::kDecMaxSplits) return FA_ERR_BAD_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_BAD_SCALE;
+    if (window > 0 && !causal) return FA_ERR_BAD_MASK;
+    const int64_t rows_q = static_cast<int64_t>(B) * Nq;
+    const int64_t rows_k = static_cast<int64_t>(B) * Nk;
+    const int group = H / Hkv;
+    if (rows_q > (int64_t{1} << 31) - 1 || rows_q * H * d > (int64_t{1} << 40) ||
+        static_cast<int64_t>(B) * Hkv * fa::kDecMaxSplits * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
+            (int64_t{1} << 31) - 1)
+        return FA_ERR_BAD_SHAPE;
+    if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
+    if (misaligned(q) || misaligned(k_codes) || misaligned(k_words) || misaligned(v_codes) ||
+        misaligned(v_words) || misaligned(o) || misaligned(lse) ||
+        (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
+        return FA_ERR_MISALIGNED;
+    if (rows_q == 0) return FA_OK;
+    auto check_ws = [&](int ns) {
+        const size_t need = kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, ns);
+        if (need == 0) return FA_OK;
+        if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+        return misaligned(workspace) ? FA_ERR_MISALIGNED : FA_OK;
+    };
+    int rc = num_splits > 0 ? check_ws(num_splits) : FA_OK;
+    if (rc != FA_OK) return rc;
+    DeviceState* st = nullptr;
+    if ((rc = device_setup(&st)) != FA_OK) return rc;
+    const int ns = num_splits > 0 ? num_splits : kv4_splits(B, H, Hkv, Nq, Nk, st->num_sms);
+    if ((rc = check_ws(ns)) != FA_OK) return rc;
+    float* part = static_cast<float*>(workspace);
+
+    if (!kv4_direct(Nq, group, Nk)) {
+        // read the rows in use back into the workspace (exactly: they are bf16
+        // numbers) and run the chunk on the tensor-core forward
+        uint8_t* back = static_cast<uint8_t*>(workspace) + decode_workspace_bytes(B, H, Nq, d, ns);
+        void* kb = back;
+        void* vb = back + kv4_readback_bytes(B, Hkv, Nk, d);
+        fa::Kv4Params r = {};
+        r.place.lens = seqlens_k;
+        r.place.B = B;
+        r.place.N = Nk;
+        r.place.H = Hkv;
+        r.place.Nk = Nk;
+        r.place.from_window = window > 0 ? window : 0;
+        r.place.from_queries = Nq;
+        r.rows = rows_k;
+        r.x[0] = static_cast<__nv_bfloat16*>(kb);
+        r.x[1] = static_cast<__nv_bfloat16*>(vb);
+        r.codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+        r.codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+        r.words[0] = static_cast<uint16_t*>(const_cast<void*>(k_words));
+        r.words[1] = static_cast<uint16_t*>(const_cast<void*>(v_words));
+        r.poison = 1;
+        rc = d == 64 ? launch_kv4_rows<64, false>(r, st->num_sms, stream)
+                     : launch_kv4_rows<128, false>(r, st->num_sms, stream);
+        if (rc != FA_OK) return rc;
+        return launch_chunk(q, kb, vb, o, lse, B, H, group, Nq, Nk, d, scale, causal, window, seqlens_k, ns,
+                            part, st, stream);
+    }
+
+    fa::Kv4DecodeParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.codes[0] = static_cast<const uint8_t*>(k_codes);
+    p.codes[1] = static_cast<const uint8_t*>(v_codes);
+    p.words[0] = static_cast<const uint16_t*>(k_words);
+    p.words[1] = static_cast<const uint16_t*>(v_words);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.o_part = ns > 1 ? part : nullptr;
+    p.lse_part = ns > 1 ? part + static_cast<size_t>(ns) * rows_q * H * d : nullptr;
+    p.seqlens_k = seqlens_k;
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.G = group;
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.causal = causal ? 1 : 0;
+    p.window = window > 0 ? window : 0;
+    p.nsplit = ns;
+    p.row_blocks = static_cast<int>(kv4_row_blocks(static_cast<int64_t>(Nq) * group));
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return d == 64 ? launch_kv4_decode<64>(p, stream) : launch_kv4_decode<128>(p, stream);
 }
 
 size_t fa_fp8_vt_bytes(int B, int H, int N, int d) {

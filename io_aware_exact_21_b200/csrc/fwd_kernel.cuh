@@ -52,7 +52,8 @@
 // each item then writes O / l as fp32 and the base-2 log-sum-exp of its range
 // to the split buffers ([nsplit, rows, H, D] and [nsplit, H, rows]), which
 // combine_kernel merges.  A split with no tiles writes -inf and is skipped by
-// the merge.  Cache rows past a sequence's used length are never read: K and V
+// the merge.  Query head h reads key/value head h / group (group = 1 where
+// every query head has its own).  Cache rows past a sequence's used length are never read: K and V
 // come through 4-D maps [B, Nk, H, d] (coordinates channel, head, row,
 // sequence), and a key tile that would reach past the used length nk is read
 // right-aligned instead, as keys [nk - 128, nk) -- rows before 0 are outside
@@ -95,6 +96,7 @@ struct FwdParams {
         const int* seqused_k;   // or nullptr (all Nk rows in use)
         float* o_part;          // [nsplit, B * N, H, D]
         float* lse_part;        // [nsplit, H, B * N], base 2
+        int group;              // query heads to a key/value head (the maps' heads: H / group)
     };
     union {
         F8 f8;
@@ -267,6 +269,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                     split = h % p.nsplit;
                     h /= p.nsplit;
                 }
+                [[maybe_unused]] const int hk = kCache ? h / p.kv.group : h;
                 const SeqSpan sp = sch.span(s);
                 const SeqSpan kp = kCache ? sch.kspan_used(s, p.kv.seqused_k) : sch.kspan(s);
                 const int off = kp.len - sp.len;        // key position of query row 0
@@ -316,7 +319,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                                 const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
                                 const int k0 = cache_tile_key0(j, kp.len);
                                 for (int b = 0; b < C::NBOX; ++b)
-                                    tma_load_4d(dst + b * C::BOX_BYTES, tm, full, b * 128 / C::ESIZE, h,
+                                    tma_load_4d(dst + b * C::BOX_BYTES, tm, full, b * 128 / C::ESIZE, hk,
                                                 k0, s);
                             } else {
                                 const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
@@ -700,8 +703,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                     }
                 }
                 if (valid)
+                    // (a NaN sum stays NaN, so that the merge does not pass over this split)
                     p.kv.lse_part[(static_cast<size_t>(split) * H + h) * p.g.T + sp.start + i] =
-                        l > 0.f ? m_ref + __log2f(l) : -INFINITY;
+                        l == 0.f ? -INFINITY : m_ref + __log2f(l);
                 tc_fence_before();
                 continue;
             }

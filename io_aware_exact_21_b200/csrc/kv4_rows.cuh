@@ -1,0 +1,271 @@
+// kv4_rows.cuh -- the 4-bit key/value cache: its number format, and the
+// kernels that write new rows into it and read rows back.
+//
+// A cache row is one token of one key/value head, x of D channels.  With
+//     hi = max(0, max x),  lo = min(0, min x),
+//     s  = the smallest number with 4 significant bits that has
+//          15 s >= hi - lo (and is at least 2^-126),
+//     z  = floor(-lo / s + 1/2)                                 (0 .. 15),
+//     c  = min(15, floor(x / s + 1/2) + z)                      (0 .. 15)
+// it stands for s (c - z), at most s / 2 away from x.  s has 4 significant
+// bits and |c - z| <= 15 has 4, so every value is a bf16 number: reading a
+// row back, and attention over the rows read back, round nothing.  s is bf16
+// with its low four mantissa bits zero, and those four bits hold z: one
+// 16-bit word a row, 4 + 16/D bits a value.  A row that holds NaN or infinity
+// gets s = NaN and reads back as NaN.
+//
+// Both kernels move each byte once and compute little, so HBM bounds them:
+// 2 D bytes of bf16 against D / 2 + 2 of cache for a row.  A row's D / 8
+// lanes hold 8 channels each (one 16-byte access of the bf16 side, one 4-byte
+// access of the codes); a warp takes consecutive tokens of one head, so that
+// its cache rows lie next to each other, and starts all its loads before it
+// uses the first.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace fa {
+
+constexpr uint32_t kKv4NaN = 0x7fc0u;     // the word of a row that holds NaN or infinity
+
+// Where the rows of a write or read sit: row i of sequence b, i < n_b, is
+// cache row starts[b] + i.  n_b is N, or lens[b] where that is smaller; with
+// cu_seqlens the rows are packed and n_b is cu_seqlens[b + 1] - cu_seqlens[b].
+struct Kv4Place {
+    const int* cu_seqlens;   // or nullptr
+    const int* starts;       // or nullptr (all 0)
+    const int* lens;         // or nullptr (all N)
+    int B, N, H;             // N: rows a sequence; packed: all rows
+    int Nk;                  // cache rows a sequence has room for
+    int from_window;         // > 0: rows of positions that no query of the
+    int from_queries;        //   attention call needs are left out (see first_row)
+};
+
+// For attention under a sliding window: the first cache row that the last
+// `from_queries` positions of a sequence of n rows read, with the 128-key tile
+// that holds it and the last (right-aligned) tile whole.
+__device__ __forceinline__ int kv4_first_row(const Kv4Place& w, int n) {
+    if (w.from_window <= 0) return 0;
+    const int64_t first = static_cast<int64_t>(n) - w.from_queries - w.from_window + 1;
+    if (first <= 0) return 0;
+    return max(0, min(static_cast<int>(first) / 128 * 128, n - 128));
+}
+
+// Sequence and cache row of row r of the [rows, H, D] side; false when r
+// belongs to no sequence or its cache row does not exist.
+__device__ __forceinline__ bool kv4_place(const Kv4Place& w, int64_t r, int64_t rows, int& b, int& pos) {
+    if (r >= rows) return false;
+    int64_t i;
+    if (w.cu_seqlens) {
+        if (w.B <= 0 || r >= w.cu_seqlens[w.B] || r < w.cu_seqlens[0]) return false;
+        int lo = 0, hi = w.B;                 // cu[lo] <= r < cu[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (w.cu_seqlens[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        i = r - w.cu_seqlens[b];
+    } else {
+        b = static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(w.N));   // rows < 2^31
+        i = r - static_cast<int64_t>(b) * w.N;
+        const int n = w.lens ? min(w.lens[b], w.N) : w.N;
+        if (i >= n || i < kv4_first_row(w, n)) return false;
+    }
+    const int64_t at = (w.starts ? w.starts[b] : 0) + i;
+    pos = static_cast<int>(at);
+    return at >= 0 && at < w.Nk;
+}
+
+__device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Codes of 8 channels (one bf16 pair a word) of a row, and the row's word.
+// LANES neighbouring lanes hold the row.
+//
+// s: hi - lo rounded up to fp32 and divided by 15 rounding up, then rounded up
+// to 4 significant bits.  15 s and s are fp32 numbers, so comparing them with
+// a value rounded up decides as the exact value does.  (Halved first, so that
+// the sum cannot overflow.)
+//
+// c: x / s is either exactly half-way between two integers or at least 2^-10
+// away from that (8 bits over 4 bits), while x * (1 / s) + z errs by less than
+// 2^-18; so adding 1/2 + 2^-11 before cutting the fraction gives the nearest
+// integer with exact ties upwards.  Adding 128 as well puts the integer into
+// the third byte of the fp32 pattern, from where byte permutes collect it.
+template <int LANES>
+__device__ __forceinline__ uint32_t kv4_encode(const uint4& x, uint32_t& word) {
+    constexpr uint32_t kSign = 0x80008000u;
+    uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
+    uint32_t dn = bf2_max_nan(bf2_max_nan(x.x ^ kSign, x.y ^ kSign), bf2_max_nan(x.z ^ kSign, x.w ^ kSign));
+    // low half: the larger value of `up`'s halves, high half: of `dn`'s
+    uint32_t m = bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = bf2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = bf2_max_nan(m, 0u);
+    const float hi = __uint_as_float(m << 16), neg_lo = __uint_as_float(m & 0xffff0000u);
+    const float y = __fdiv_ru(__fadd_ru(0.5f * hi, 0.5f * neg_lo), 7.5f);
+    const uint32_t sb = max((__float_as_uint(y) + 0x000fffffu) & 0xfff00000u, 0x00800000u);
+    if (!(hi <= 3.4e38f && neg_lo <= 3.4e38f)) {
+        word = kKv4NaN;
+        return 0u;
+    }
+    const float inv = __frcp_rn(__uint_as_float(sb));
+    constexpr float kHalfUp = 0.5f + 1.f / 2048.f;
+    const float z = floorf(fmaf(neg_lo, inv, kHalfUp));
+    word = (sb >> 16) | static_cast<uint32_t>(z);
+    const float base = 128.f + kHalfUp + z;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    uint32_t e[4], o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = fmaf(__uint_as_float(xs[j] << 16), inv, base);
+        const float b = fmaf(__uint_as_float(xs[j] & 0xffff0000u), inv, base);
+        e[j] = __float_as_uint(fminf(a, 143.9f));
+        o[j] = __float_as_uint(fminf(b, 143.9f));
+    }
+    const uint32_t even = __byte_perm(__byte_perm(e[0], e[1], 0x0062), __byte_perm(e[2], e[3], 0x0062), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(o[0], o[1], 0x0062), __byte_perm(o[2], o[3], 0x0062), 0x5410);
+    return even | (odd << 4);
+}
+
+// The 8 channels of a word of codes as bf16.  128 + c - (128 + z) and the
+// product with s are exact.
+__device__ __forceinline__ uint4 kv4_decode(uint32_t codes, uint32_t word) {
+    const uint32_t s2 = (word & 0xfff0u) * 0x00010001u;
+    const uint32_t z2 = (0xc300u | (word & 15u)) * 0x00010001u;       // -(128 + z), twice
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t byte = (codes >> (8 * j)) & 0xffu;
+        const uint32_t c2 = ((byte * 4097u) & 0x000f000fu) | 0x43004300u;   // 128 + c, low and high code
+        uint32_t d, v;
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(c2), "r"(z2));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(d), "r"(s2));
+        r[j] = v;
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+struct Kv4Params {
+    Kv4Place place;
+    int64_t rows;                  // rows of the bf16 side
+    __nv_bfloat16* x[2];           // K, V: [rows, H, D]
+    uint8_t* codes[2];             // [B, H, Nk, D / 2]
+    uint16_t* words[2];            // [B, H, Nk]
+    int poison;                    // reading for attention: see kv4_read_kernel
+};
+
+constexpr int kKv4Warps = 8;
+
+// Tokens that one warp takes: ITER steps of the 32 / (D / 8) rows it holds at once.
+template <int D, int ITER>
+__host__ __device__ constexpr int kv4_tokens() { return ITER * (32 / (D / 8)); }
+
+// Sequence and cache row of each of a warp's tokens: lane j holds token j's
+// (pos < 0: not taken).
+template <int TOK>
+__device__ __forceinline__ void kv4_warp_places(const Kv4Params& p, int64_t first, int& b, int& pos) {
+    const int lane = lane_id();
+    b = 0;
+    pos = -1;
+    if (lane < TOK) {
+        int bb, pp;
+        if (kv4_place(p.place, first + lane, p.rows, bb, pp)) {
+            b = bb;
+            pos = pp;
+        }
+    }
+}
+
+// Writes bf16 rows into the cache.  blockIdx.y selects K or V.
+template <int D, int ITER>
+__global__ void __launch_bounds__(kKv4Warps * 32)
+kv4_write_kernel(const Kv4Params p) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, TOK = kv4_tokens<D, ITER>();
+    const int lane = lane_id();
+    const int H = p.place.H;
+    const uint32_t unit = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);    // the host keeps units below 2^31
+    const uint32_t chunk = unit / static_cast<uint32_t>(H);
+    const int h = static_cast<int>(unit - chunk * H);
+    const int64_t first = static_cast<int64_t>(chunk) * TOK;
+    if (first >= p.rows) return;
+    const __nv_bfloat16* x = blockIdx.y ? p.x[1] : p.x[0];
+    uint8_t* codes = blockIdx.y ? p.codes[1] : p.codes[0];
+    uint16_t* words = blockIdx.y ? p.words[1] : p.words[0];
+    const int sub = lane / LANES, c8 = lane % LANES;
+    uint4 v[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+        const int64_t r = first + it * ROWS + sub;
+        v[it] = r < p.rows ? __ldcs(reinterpret_cast<const uint4*>(x + (r * H + h) * D + c8 * 8))
+                           : make_uint4(0, 0, 0, 0);
+    }
+    int tb, tpos;
+    kv4_warp_places<TOK>(p, first, tb, tpos);
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+        uint32_t word;
+        const uint32_t c = kv4_encode<LANES>(v[it], word);
+        const int b = __shfl_sync(0xffffffffu, tb, it * ROWS + sub);
+        const int pos = __shfl_sync(0xffffffffu, tpos, it * ROWS + sub);
+        if (pos >= 0) {
+            const int64_t row = (static_cast<int64_t>(b) * H + h) * p.place.Nk + pos;
+            *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + c8 * 4) = c;
+            if (c8 == 0) words[row] = static_cast<uint16_t>(word);
+        }
+    }
+}
+
+// Reads cache rows back as bf16.  poison (attention's own use): a token whose
+// K or V row is NaN becomes K = NaN, V = 0, so that it reaches the scores of
+// the queries that see it and no product of the others (0 * NaN).
+template <int D, int ITER>
+__global__ void __launch_bounds__(kKv4Warps * 32)
+kv4_read_kernel(const Kv4Params p) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, TOK = kv4_tokens<D, ITER>();
+    const int lane = lane_id();
+    const int H = p.place.H;
+    const uint32_t unit = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);    // the host keeps units below 2^31
+    const uint32_t chunk = unit / static_cast<uint32_t>(H);
+    const int h = static_cast<int>(unit - chunk * H);
+    const int64_t first = static_cast<int64_t>(chunk) * TOK;
+    if (first >= p.rows) return;
+    const uint8_t* codes = blockIdx.y ? p.codes[1] : p.codes[0];
+    const uint16_t* words = blockIdx.y ? p.words[1] : p.words[0];
+    const uint16_t* other = blockIdx.y ? p.words[0] : p.words[1];
+    __nv_bfloat16* x = blockIdx.y ? p.x[1] : p.x[0];
+    const int sub = lane / LANES, c8 = lane % LANES;
+    int tb, tpos;
+    kv4_warp_places<TOK>(p, first, tb, tpos);
+    uint32_t c[ITER], word[ITER];
+    bool taken[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+        const int b = __shfl_sync(0xffffffffu, tb, it * ROWS + sub);
+        const int pos = __shfl_sync(0xffffffffu, tpos, it * ROWS + sub);
+        taken[it] = pos >= 0;
+        c[it] = word[it] = 0;
+        if (taken[it]) {
+            const int64_t row = (static_cast<int64_t>(b) * H + h) * p.place.Nk + pos;
+            c[it] = *reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + c8 * 4);
+            word[it] = words[row];
+            if (p.poison) {
+                const bool nan = word[it] >= 0x7f80u || other[row] >= 0x7f80u;
+                if (nan) word[it] = blockIdx.y == 0 ? kKv4NaN : 0u;
+            }
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+        if (taken[it]) {
+            const int64_t r = first + it * ROWS + sub;
+            *reinterpret_cast<uint4*>(x + (r * H + h) * D + c8 * 8) = kv4_decode(c[it], word[it]);
+        }
+    }
+}
+
+}  // namespace fa
