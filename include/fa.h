@@ -230,11 +230,13 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  *   Up to 32 query rows to a key/value head (Nq * H / Hkv) run on a kernel
  * that multiplies the 4-bit codes as they are; more are run by reading the
  * rows in use back into the workspace for the tensor-core forward.
- *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, splits) bytes,
- * 16-byte aligned (0, then NULL is allowed, for few rows and one split);
- * contents on entry do not matter.  Calls that may overlap on the GPU need
- * one each.  num_splits as fa_fwd_kvcache, 0 for fa_fwd_kv4_num_splits's
- * choice.
+ *   num_splits : few rows: 1 gives every (sequence, key/value head) one CTA,
+ * more cut the keys of all of them together into num_splits equal ranges to
+ * each; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.
+ *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
+ * bytes (of the current device, for num_splits = 0), 16-byte aligned (0 bytes,
+ * and NULL allowed, for few rows and one split); contents on entry do not
+ * matter.  Calls that may overlap on the GPU need one each.
  * Errors as fa_fwd_kvcache; H not a multiple of Hkv is FA_ERR_BAD_SHAPE.
  */
 int fa_quantize_kv4(const void* k, const void* v, void* k_codes, void* k_words, void* v_codes,
@@ -244,7 +246,6 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
                       const void* v_words, void* k, void* v, int B, int N, int Hkv, int Nk, int d,
                       const int* cu_seqlens, const int* starts, const int* lens,
                       cudaStream_t stream);
-int fa_fwd_kv4_num_splits(int B, int H, int Hkv, int Nq, int Nk, int d);
 size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits);
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
                const void* v_words, void* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,

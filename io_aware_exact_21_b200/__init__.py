@@ -8,7 +8,7 @@
 from .binding import (FaError, backward, dequantize_kv4, fa_bwd, fa_bwd_fused, fa_bwd_fused_workspace_size,
                       fa_bwd_noalloc, fa_bwd_workspace_size,
                       fa_debug_set_fault, fa_dequantize_kv4, fa_fp8_vt_bytes, fa_fwd, fa_fwd_fp8, fa_fwd_kv,
-                      fa_fwd_kv4, fa_fwd_kv4_num_splits, fa_fwd_kv4_workspace_size,
+                      fa_fwd_kv4, fa_fwd_kv4_workspace_size,
                       fa_fwd_kvcache, fa_quantize_fp8, fa_quantize_kv4, forward_fp8, quantize_fp8,
                       fa_fwd_kvcache_num_splits, fa_fwd_kvcache_workspace_size,
                       fa_get_device_error, fa_profile_begin, fa_profile_cta_balance, fa_profile_end, fa_status_string,
@@ -18,7 +18,7 @@ from .binding import (FaError, backward, dequantize_kv4, fa_bwd, fa_bwd_fused, f
 __all__ = ["FaError", "backward", "dequantize_kv4", "fa_bwd", "fa_bwd_fused", "fa_bwd_fused_workspace_size",
            "fa_bwd_noalloc", "fa_bwd_workspace_size",
            "fa_debug_set_fault", "fa_dequantize_kv4", "fa_fp8_vt_bytes", "fa_fwd", "fa_fwd_fp8", "fa_fwd_kv",
-           "fa_fwd_kv4", "fa_fwd_kv4_num_splits", "fa_fwd_kv4_workspace_size",
+           "fa_fwd_kv4", "fa_fwd_kv4_workspace_size",
            "fa_fwd_kvcache", "fa_quantize_fp8", "fa_quantize_kv4", "forward_fp8", "quantize_fp8",
            "fa_fwd_kvcache_num_splits", "fa_fwd_kvcache_workspace_size", "fa_get_device_error",
            "fa_profile_begin", "fa_profile_cta_balance", "fa_profile_end", "fa_status_string", "forward", "forward_kv", "forward_kv4",

@@ -39,7 +39,6 @@ SIGNATURES = {
                                _VP]),
     "fa_fwd_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP,
                         _I, _VP, _SZ, _VP]),
-    "fa_fwd_kv4_num_splits": (_I, [_I, _I, _I, _I, _I, _I]),
     "fa_fwd_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _I,
@@ -175,11 +174,6 @@ def fa_fwd_kv4(q, k_codes, k_words, v_codes, v_words, o, lse, B, H, Hkv, Nq, Nk,
                                      int(Nq), int(Nk), int(d), float(scale), int(causal),
                                      int(window), _ptr(seqlens_k), int(num_splits),
                                      _ptr(workspace), int(workspace_bytes), _stream(stream))
-
-
-def fa_fwd_kv4_num_splits(B, H, Hkv, Nq, Nk, d) -> int:
-    return int(load_library().fa_fwd_kv4_num_splits(int(B), int(H), int(Hkv), int(Nq), int(Nk),
-                                                    int(d)))
 
 
 def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits) -> int:
@@ -558,14 +552,13 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
     _expect(out, "out", q.shape, torch.bfloat16, dev)
     _expect(lse, "lse", (B, H, Nq), torch.float32, dev)
-    ns = num_splits if num_splits > 0 else fa_fwd_kv4_num_splits(B, H, Hkv, Nq, Nk, d)
-    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, ns)
+    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, dev)
     _check(fa_fwd_kv4(q, *(cache[n] for n in KV4_NAMES), out, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
-                      window, seqlens_k, ns, workspace, 0 if workspace is None else workspace.numel(),
+                      window, seqlens_k, num_splits, workspace, 0 if workspace is None else workspace.numel(),
                       stream), "fa_fwd_kv4")
     return out, lse
 

@@ -458,28 +458,21 @@ int64_t kv4_row_blocks(int64_t rows) {
     return (rows + per - 1) / per;
 }
 
-// Split count of kv4_decode_kernel: as decode_splits, for its CTAs an SM and
-// at least 256 keys a split.
-int kv4_splits(int B, int H, int Hkv, int Nq, int Nk, int num_sms) {
-    const int group = H / Hkv;
-    if (!kv4_direct(Nq, group, Nk)) return prefill_splits(B, H, Nq, Nk, num_sms);
+// Ranges that kv4_decode_kernel cuts its work into (0: a CTA to each item and
+// no merge).
+int kv4_range_count(int B, int Hkv, int Nq, int group, int Nk, int num_splits, int num_sms) {
     const int64_t rows = static_cast<int64_t>(Nq) * group;
     const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
-    const int max_ns = std::max(1, std::min(fa::kDecMaxSplits, (Nk + 255) / 256));
-    const int64_t slots = (kv4_block_rows(rows) == 8 ? 2 : 3) * static_cast<int64_t>(num_sms);
-    int best = 1;
-    double best_fill = -1.0;
-    for (int ns = 1; ns <= max_ns; ++ns) {
-        const int64_t ctas = items * ns;
-        const int64_t waves = (ctas + slots - 1) / slots;
-        const double fill = static_cast<double>(ctas) / static_cast<double>(waves * slots);
-        if (fill >= 0.9) return ns;
-        if (fill > best_fill + 1e-9) {
-            best_fill = fill;
-            best = ns;
-        }
-    }
-    return best;
+    if (num_splits == 1 || Nk == 0) return 0;
+    if (num_splits > 1) return static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20));
+    return 3 * num_sms;
+}
+
+int current_sms() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 148;
 }
 
 // Bytes of the bf16 K (and of the V) that a chunk is read back into.
@@ -488,8 +481,19 @@ size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
     return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
-size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int ns) {
-    const size_t part = decode_workspace_bytes(B, H, Nq, d, ns);
+// Bytes of the partial results: of the ranges (two of ROWS rows, each with its
+// maximum and sum), or of a chunk's splits.
+size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits, int num_sms) {
+    const int group = H / Hkv;
+    if (!kv4_direct(Nq, group, Nk))
+        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
+    const size_t rows = 2 * static_cast<size_t>(kv4_range_count(B, Hkv, Nq, group, Nk, num_splits, num_sms)) *
+                        kv4_block_rows(static_cast<int64_t>(Nq) * group);
+    return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits, int num_sms) {
+    const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, num_splits, num_sms);
     return kv4_direct(Nq, H / Hkv, Nk) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
 }
 
@@ -565,23 +569,28 @@ int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_wo
 }
 
 template <int D, int NT>
-cudaError_t launch_kv4_decode_nt(const fa::Kv4DecodeParams& p, int grid, cudaStream_t stream) {
-    using C = fa::Kv4DecCfg<D, NT>;
-    fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(p);
-    return cudaGetLastError();
-}
-
-template <int D>
 int launch_kv4_decode(const fa::Kv4DecodeParams& p, cudaStream_t stream) {
-    const int grid = p.B * p.Hkv * p.nsplit * p.row_blocks;
+    using C = fa::Kv4DecCfg<D, NT>;
+    const int items = p.B * p.Hkv * p.row_blocks;
     const int slot = prof_start(4, stream);
-    const cudaError_t e = kv4_block_rows(static_cast<int64_t>(p.Nq) * p.G) == 8
-                              ? launch_kv4_decode_nt<D, 1>(p, grid, stream)
-                              : launch_kv4_decode_nt<D, 2>(p, grid, stream);
+    fa::kv4_decode_kernel<D, NT><<<p.ranges > 0 ? p.ranges : items, C::WARPS * 32, C::SMEM, stream>>>(p);
     prof_stop(4, slot, stream);
-    if (e != cudaSuccess) return FA_ERR_CUDA;
-    return p.nsplit > 1 ? launch_combine<D>(p.o_part, p.lse_part, p.o, p.lse, p.B, p.H, p.Nq, p.nsplit, stream)
-                        : FA_OK;
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (p.ranges == 0) return FA_OK;
+    const int slot2 = prof_start(5, stream);
+    // programmatic dependent launch, as the merge of the bf16 decode
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Nq * p.H));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::kv4_merge_kernel<D, NT>, p);
+    prof_stop(5, slot2, stream);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // ------------------------------------------------ allocation-free backward --
@@ -820,19 +829,9 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
                            lens, stream);
 }
 
-int fa_fwd_kv4_num_splits(int B, int H, int Hkv, int Nq, int Nk, int d) {
-    (void)d;
-    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nk <= 0 || Nq <= 0) return 1;
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (sms <= 0) sms = 148;
-    return kv4_splits(B, H, Hkv, Nq, Nk, sms);
-}
-
 size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits) {
-    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0) return 0;
-    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, num_splits);
+    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0 || num_splits < 0) return 0;
+    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, num_splits, current_sms());
 }
 
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
@@ -849,6 +848,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     const int64_t rows_k = static_cast<int64_t>(B) * Nk;
     const int group = H / Hkv;
     if (rows_q > (int64_t{1} << 31) - 1 || rows_q * H * d > (int64_t{1} << 40) ||
+        (kv4_direct(Nq, group, Nk) && rows_q * H > (int64_t{1} << 31) - 1) ||
         static_cast<int64_t>(B) * Hkv * fa::kDecMaxSplits * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
             (int64_t{1} << 31) - 1)
         return FA_ERR_BAD_SHAPE;
@@ -858,23 +858,18 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
         return FA_ERR_MISALIGNED;
     if (rows_q == 0) return FA_OK;
-    auto check_ws = [&](int ns) {
-        const size_t need = kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, ns);
-        if (need == 0) return FA_OK;
-        if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
-        return misaligned(workspace) ? FA_ERR_MISALIGNED : FA_OK;
-    };
-    int rc = num_splits > 0 ? check_ws(num_splits) : FA_OK;
-    if (rc != FA_OK) return rc;
+    const size_t need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+    if (need > 0 && misaligned(workspace)) return FA_ERR_MISALIGNED;
     DeviceState* st = nullptr;
-    if ((rc = device_setup(&st)) != FA_OK) return rc;
-    const int ns = num_splits > 0 ? num_splits : kv4_splits(B, H, Hkv, Nq, Nk, st->num_sms);
-    if ((rc = check_ws(ns)) != FA_OK) return rc;
+    int rc = device_setup(&st);
+    if (rc != FA_OK) return rc;
     float* part = static_cast<float*>(workspace);
 
     if (!kv4_direct(Nq, group, Nk)) {
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
+        const int ns = num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, st->num_sms);
         uint8_t* back = static_cast<uint8_t*>(workspace) + decode_workspace_bytes(B, H, Nq, d, ns);
         void* kb = back;
         void* vb = back + kv4_readback_bytes(B, Hkv, Nk, d);
@@ -909,8 +904,6 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.words[1] = static_cast<const uint16_t*>(v_words);
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.o_part = ns > 1 ? part : nullptr;
-    p.lse_part = ns > 1 ? part + static_cast<size_t>(ns) * rows_q * H * d : nullptr;
     p.seqlens_k = seqlens_k;
     p.B = B;
     p.H = H;
@@ -920,10 +913,17 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.Nk = Nk;
     p.causal = causal ? 1 : 0;
     p.window = window > 0 ? window : 0;
-    p.nsplit = ns;
-    p.row_blocks = static_cast<int>(kv4_row_blocks(static_cast<int64_t>(Nq) * group));
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    p.row_blocks = static_cast<int>(kv4_row_blocks(rows));
+    p.ranges = kv4_range_count(B, Hkv, Nq, group, Nk, num_splits, st->num_sms);
+    p.o_part = part;
+    p.ml_part = reinterpret_cast<float2*>(part + 2 * static_cast<size_t>(p.ranges) * kv4_block_rows(rows) * d);
     p.scale_log2 = scale * 1.4426950408889634f;
-    return d == 64 ? launch_kv4_decode<64>(p, stream) : launch_kv4_decode<128>(p, stream);
+    p.error_word = st->error_word;
+    p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
+    if (d == 64)
+        return kv4_block_rows(rows) == 8 ? launch_kv4_decode<64, 1>(p, stream) : launch_kv4_decode<64, 2>(p, stream);
+    return kv4_block_rows(rows) == 8 ? launch_kv4_decode<128, 1>(p, stream) : launch_kv4_decode<128, 2>(p, stream);
 }
 
 size_t fa_fp8_vt_bytes(int B, int H, int N, int d) {

@@ -27,10 +27,12 @@
 // unpacked, while tcgen05 would have them written back to shared or tensor
 // memory as 16-bit words first, four times the cache's bytes.
 //
-// One warp is on its own: it takes every WARPS-th tile of 32 keys of the
-// CTA's range through its own ring of cp.async stages, with its own running
-// maximum and sums, so the key loop has no CTA barrier; the warps' results
-// merge once at the end, the splits' in combine_kernel.
+// The key tiles of all heads and sequences are cut into equal ranges, one a
+// CTA (kv4_span below).  In a range one warp is on its own: it takes every
+// WARPS-th tile of 32 keys through its own ring of bulk copies, with its own
+// running maximum and sums, so the key loop has no CTA barrier; the warps'
+// results merge at the end of an item, those of an item that lies in several
+// ranges in kv4_merge_kernel.
 //
 // Per tile: S^T = C^k q^T with 16 keys x 8 query rows to an mma (the codes are
 // the A operand), p from it in registers, transposed by movmatrix into the B
@@ -51,21 +53,26 @@ struct Kv4DecodeParams {
     const uint16_t* words[2];    // [B, Hkv, Nk]
     __nv_bfloat16* o;            // [B, Nq, H, D]
     float* lse;                  // [B, H, Nq]
-    float* o_part;               // nsplit > 1: [nsplit, B * Nq, H, D]
-    float* lse_part;             // nsplit > 1: [nsplit, H, B * Nq], base 2
+    float* o_part;               // ranges > 0: [2 ranges, ROWS, D], see kv4_range
+    float2* ml_part;             // ranges > 0: [2 ranges, ROWS] (maximum, sum), base 2
     const int* seqlens_k;        // [B] or nullptr
     int B, H, Hkv, G, Nq, Nk;    // G = H / Hkv
-    int causal, window, nsplit, row_blocks;
+    int causal, window;
+    int row_blocks;              // blocks of ROWS query rows to a (sequence, kv head)
+    int ranges;                  // ranges the work is cut into; 0: a CTA to each item
     float scale_log2;
+    int* error_word;
+    uint64_t timeout_ns;
 };
 
 template <int D, int NT>
 struct Kv4DecCfg {
-    static constexpr int BN = 32;                         // keys a tile
+    static constexpr int BN = NT == 1 ? 64 : 32;          // keys a tile
     static constexpr int ROWS = 8 * NT;                   // query rows a CTA
-    static constexpr int WARPS = NT == 1 ? 8 : 4;
-    static constexpr int MIN_CTAS = NT == 1 ? 2 : 3;
-    static constexpr int NSTAGE = 3;
+    static constexpr int WARPS = 4;
+    static constexpr int MIN_CTAS = 3;
+    static constexpr int NSTAGE = NT == 1 ? 2 : 4;
+    static constexpr int MT = BN / 16;                    // mma key tiles
     static constexpr int ROWB = D / 2;                    // bytes of a row's codes
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
@@ -73,30 +80,30 @@ struct Kv4DecCfg {
     static constexpr int RING = NSTAGE * STAGE;           // a warp's
     static constexpr int SCALES = 2 * BN * 8;             // a warp's (scale, zero) of K and V
     static constexpr int OFF_SCALES = WARPS * RING;
-    static constexpr int OFF_STATS = OFF_SCALES + WARPS * SCALES;   // max and sum [WARPS][ROWS]
-    static constexpr int SMEM = OFF_STATS + 2 * WARPS * ROWS * 4;
+    static constexpr int OFF_STATS = OFF_SCALES + WARPS * SCALES;       // float4 [WARPS][ROWS]
+    static constexpr int OFF_BAR = OFF_STATS + WARPS * ROWS * 16;       // [WARPS][NSTAGE]
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * NSTAGE * 8;
+    static constexpr int SMEM = OFF_MISC + 32 + WARPS * 4;
     static constexpr int OSTRIDE = D + 4;                 // floats a row of the merge area
-    static_assert(WARPS * ROWS * OSTRIDE * 4 <= OFF_STATS, "the merge reuses ring and scales");
-    static_assert(STAGE % 16 == 0, "16-byte copies");
+    static_assert(ROWS * OSTRIDE * 4 <= RING, "a warp leaves its partial output in its ring");
+    static_assert(STAGE % 16 == 0 && TILE % 16 == 0, "16-byte copies");
 };
 
-// 16 bytes of shared memory from global memory, `bytes` of them copied and the
-// rest zero (0: nothing is read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0].x), "=f"(c[0].y), "=f"(c[1].x), "=f"(c[1].y)
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -113,17 +120,63 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 
 constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
+constexpr float kKv4Over = 256.f;      // p may grow to this before its reference moves: 2^8 times s^v below 2^7 is in fp16
+constexpr float kNoRef = 3.4028234e38f;   // minus the reference before the first score: any score then is over
 
-// Shared-memory row of key k (0 .. 31) of a V tile.  The PV product wants keys
-// 2t, 2t + 1, 2t + 8, 2t + 9 on lane t of each four; this order (with 16-byte
-// chunks exchanged in every other pair of 64-byte rows) makes the four lanes'
-// reads of one of them fall into different banks.
-__device__ __forceinline__ int kv4_v_row(int k) {
-    return (k & 24) | ((k & 1) << 2) | ((k >> 1) & 3);
+// Key of a 16-key tile at mma index m.  K rows 2i, 2i + 1 lie in different
+// halves of a 128-byte line (64-byte rows), as the reads of two rows at a time
+// want; and of the four keys 2t that lanes t read of V together, two lie in
+// each half.
+__host__ __device__ constexpr int kv4_key(int m) { return m ^ ((m >> 1) & 1); }
+
+// ---------------------------------------------------------------- ranges --
+// The work is the sequence of all key tiles of all items, an item being a
+// (sequence, kv head, block of query rows) and `per` the items of a sequence.
+// Sequences differ in length, and only the device knows them, so the tiles are
+// cut into equal ranges, one a CTA; a range's ends may lie inside an item,
+// which then has partial results: that of the item's first tiles in slot 1 of
+// their range, all others in slot 0 of theirs (a range has at most one each).
+struct Kv4Span {
+    int nk, t0, n;      // used keys, first key tile and tiles of a sequence
+};
+
+template <int BN>
+__device__ __forceinline__ Kv4Span kv4_span(const Kv4DecodeParams& p, int b) {
+    Kv4Span s;
+    s.nk = p.seqlens_k ? min(max(p.seqlens_k[b], 0), p.Nk) : p.Nk;
+    s.t0 = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(s.nk) - p.Nq - p.window + 1)) / BN
+                        : 0;
+    s.n = (s.nk + BN - 1) / BN - s.t0;
+    return s;
 }
+
+// Ranges in use for `total` tiles: few tiles make fewer ranges than CTAs, of
+// one tile a warp at least.
+template <int WARPS>
+__device__ __forceinline__ int kv4_ranges(const Kv4DecodeParams& p, int64_t total) {
+    return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ranges), (total + WARPS - 1) / WARPS)));
+}
+
+// Index i of a lane's D / 32 values of a row as the products leave them, and
+// the channel there (channel g * D/8 + n sits at n * 8 + g).
 template <int D>
-__device__ __forceinline__ int kv4_v_chunk(int row, int chunk) {
-    return D == 128 ? chunk ^ (row & 2) : chunk;
+__device__ __forceinline__ int kv4_channel(int idx) { return (idx & 7) * (D / 8) + (idx >> 3); }
+
+// A row's output from its unnormalised values (D / 32 a lane, indices lane *
+// D/32 ..), maximum and sum.
+template <int D>
+__device__ __forceinline__ void kv4_store_row(const Kv4DecodeParams& p, int b, int hk, int r,
+                                              const float (&a)[D / 32], float M, float L) {
+    const int lane = lane_id();
+    const int i = r / p.G, h = hk * p.G + r - i * p.G;
+    const size_t row = (static_cast<size_t>(b) * p.Nq + i) * p.H + h;
+    const bool some = !(L == 0.f);              // a NaN sum stays NaN
+    const float inv = some ? 1.f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+        p.o[row * D + kv4_channel<D>(lane * (D / 32) + e)] = __float2bfloat16(a[e] * inv);
+    if (lane == 0)
+        p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = some ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, int NT>
@@ -132,399 +185,601 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     using C = Kv4DecCfg<D, NT>;
     // the merge launched after this grid may be scheduled now
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = lane_id();
     const int g8 = lane >> 2, t4 = lane & 3;
     const float kNegInf = -INFINITY;
-
-    // CTA = (sequence, kv head, split, block of query rows), the last fastest
-    int id = blockIdx.x;
-    const int rb = id % p.row_blocks;
-    id /= p.row_blocks;
-    const int split = id % p.nsplit;
-    id /= p.nsplit;
-    const int hk = id % p.Hkv;
-    const int b = id / p.Hkv;
-    const int r0 = rb * C::ROWS;                          // first of the CTA's query rows
-    const int nrows = min(C::ROWS, p.Nq * p.G - r0);
-    const int nk = p.seqlens_k ? min(max(p.seqlens_k[b], 0), p.Nk) : p.Nk;
-    const int qpos0 = nk - p.Nq;                          // key position of query 0
-    const int rows_q = p.B * p.Nq;
-
-    int tb = 0, te = 0;
-    if (!decode_split_range(nk, p.Nq, p.causal, p.window, C::BN, p.nsplit, split, tb, te)) {
-        for (int e = threadIdx.x; e < nrows; e += C::WARPS * 32) {
-            const int i = (r0 + e) / p.G, h = hk * p.G + (r0 + e) % p.G;
-            if (p.nsplit > 1)
-                p.lse_part[(static_cast<size_t>(split) * p.H + h) * rows_q + b * p.Nq + i] = kNegInf;
-            else
-                p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = kNegInf;
-        }
-        if (p.nsplit == 1)
-            for (int e = threadIdx.x; e < nrows * (D / 8); e += C::WARPS * 32) {
-                const int r = r0 + e / (D / 8);
-                const size_t row = (static_cast<size_t>(b) * p.Nq + r / p.G) * p.H + hk * p.G + r % p.G;
-                *reinterpret_cast<uint4*>(p.o + row * D + (e % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
-            }
-        return;
+    const int per = p.Hkv * p.row_blocks;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NSTAGE;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+    long long* sh_base = reinterpret_cast<long long*>(smem + C::OFF_MISC + 8);
+    int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
+    int* sh_sum = reinterpret_cast<int*>(smem + C::OFF_MISC + 32);
+    if (lane == 0) {
+        for (int s = 0; s < C::NSTAGE; ++s) mbar_init(bars + s, 1);
+        fence_barrier_init();
     }
+    if (threadIdx.x == 0) *abort_flag = 0;
 
-    // -------------------------------------------------- the warp's ring --
-    const size_t head = static_cast<size_t>(b) * p.Hkv + hk;
-    const uint8_t* kc = p.codes[0] + head * p.Nk * C::ROWB;
-    const uint8_t* vc = p.codes[1] + head * p.Nk * C::ROWB;
-    const uint16_t* kw = p.words[0] + head * p.Nk;
-    const uint16_t* vw = p.words[1] + head * p.Nk;
+    // ---------------------------------------------- this CTA's tiles --
+    // tiles [x, x_end) of the sequence; b is the sequence of tile x and `base`
+    // its first tile
+    int64_t x = 0, x_end = 0, base = 0;
+    int b = 0;
+    if (p.ranges > 0) {
+        const int each = (p.B + C::WARPS * 32 - 1) / (C::WARPS * 32);
+        const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
+        int sum = 0;
+        for (int i = b0; i < b1; ++i) sum += kv4_span<C::BN>(p, i).n;
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh_sum[warp] = incl;
+        __syncthreads();
+        int64_t total = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+            if (w == warp) before = total;
+            total += sh_sum[w];
+        }
+        total *= per;
+        const int ranges = kv4_ranges<C::WARPS>(p, total);
+        if (blockIdx.x >= ranges) return;
+        x = total * blockIdx.x / ranges;
+        x_end = total * (blockIdx.x + 1) / ranges;
+        int64_t at = (before + incl - sum) * per;
+        if (at <= x && x < at + static_cast<int64_t>(sum) * per) {
+            for (int i = b0; i < b1; ++i) {
+                const int64_t next = at + static_cast<int64_t>(kv4_span<C::BN>(p, i).n) * per;
+                if (x < next) {
+                    *sh_b = i;
+                    *sh_base = at;
+                    break;
+                }
+                at = next;
+            }
+        }
+        __syncthreads();
+        if (x >= x_end) return;
+        b = *sh_b;
+        base = *sh_base;
+    } else {
+        // item blockIdx.x alone
+        b = blockIdx.x / per;
+        const Kv4Span s = kv4_span<C::BN>(p, b);
+        const int item = blockIdx.x - b * per;
+        if (s.n == 0) {
+            const int hk = item / p.row_blocks, r0 = (item - hk * p.row_blocks) * C::ROWS;
+            const float zero[D / 32] = {};
+            for (int r = r0 + warp; r < min(r0 + C::ROWS, p.Nq * p.G); r += C::WARPS)
+                kv4_store_row<D>(p, b, hk, r, zero, kNegInf, 0.f);
+            return;
+        }
+        x = static_cast<int64_t>(item) * s.n;
+        x_end = x + s.n;
+        __syncthreads();
+    }
+    const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
     uint8_t* ring = smem + warp * C::RING;
-    const uint32_t ring_a = smem_u32(ring);
-    auto load_tile = [&](int tile, int slot) {
-        const int k0 = tile * C::BN;
-        const uint32_t dst = ring_a + slot * C::STAGE;
-        constexpr int CH = C::ROWB / 16;                  // 16-byte chunks a row
-#pragma unroll
-        for (int j = 0; j < C::BN * CH / 32; ++j) {
-            const int idx = lane + 32 * j;
-            const int key = idx / CH, chunk = idx % CH;
-            const int bytes = k0 + key < nk ? 16 : 0;
-            const size_t off = bytes ? static_cast<size_t>(k0 + key) * C::ROWB + chunk * 16 : 0;
-            cp_async16(dst + idx * 16, kc + off, bytes);
-            const int vr = kv4_v_row(key);
-            cp_async16(dst + C::TILE + vr * C::ROWB + kv4_v_chunk<D>(vr, chunk) * 16, vc + off, bytes);
-        }
-        if (lane < 8) {                                   // words: 8 keys a copy, K on lanes 0-3, V on 4-7
-            const int key = (lane & 3) * 8;
-            const int bytes = max(0, min(16, 2 * (nk - k0 - key)));
-            const uint16_t* src = (lane < 4 ? kw : vw) + (bytes ? k0 + key : 0);
-            cp_async16(dst + 2 * C::TILE + (lane >> 2) * C::WORDB + key * 2, src, bytes);
-        }
-    };
-    const int first = tb + warp;
-    const int ntile = first < te ? (te - first + C::WARPS - 1) / C::WARPS : 0;
-#pragma unroll
-    for (int s = 0; s < C::NSTAGE - 1; ++s) {
-        if (s < ntile) load_tile(first + s * C::WARPS, s);
-        cp_async_commit();
-    }
-
-    // ----------------------------------------- queries as B fragments --
-    // Row nt * 8 + g8, channels t4 * D/4 ..: of word w (8 codes), pair u of
-    // k-step pairs: codes (2u, 2u + 4) plain and (2u + 1, 2u + 5) times 1/16.
-    constexpr int W = D / 32;
-    uint32_t qf[NT][W][2][2];
-    float sq[NT][2], rf[NT][2];     // of rows nt * 8 + 2 t4 + {0, 1}: sum of q and the score factor
-    int hi[NT][2], lo[NT][2];       // their allowed keys are [lo, hi)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int rr = nt * 8 + g8;
-        uint4 raw[W];
-        const bool have = rr < nrows;
-        const size_t qrow = have ? (static_cast<size_t>(b) * p.Nq + (r0 + rr) / p.G) * p.H + hk * p.G + (r0 + rr) % p.G : 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            raw[w] = have ? *reinterpret_cast<const uint4*>(p.q + qrow * D + t4 * (D / 4) + w * 8) : make_uint4(0, 0, 0, 0);
-        uint32_t top = 0;               // largest magnitude, as bf16 bits (NaN and infinity on top)
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7fffu, (x[j] >> 16) & 0x7fffu));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(static_cast<int>(top >> 7), 14);             // biased exponent
-        const float qs = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float f[8] = {bf16_lo(raw[w].x) * qs, bf16_hi(raw[w].x) * qs, bf16_lo(raw[w].y) * qs,
-                                bf16_hi(raw[w].y) * qs, bf16_lo(raw[w].z) * qs, bf16_hi(raw[w].z) * qs,
-                                bf16_lo(raw[w].w) * qs, bf16_hi(raw[w].w) * qs};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += f[j];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                qf[nt][w][u][0] = pack_f16(f[2 * u], f[2 * u + 4]);
-                qf[nt][w][u][1] = pack_f16(f[2 * u + 1] * 0.0625f, f[2 * u + 5] * 0.0625f);
-            }
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= 5.9604644775390625e-8f;                                 // 2^-24, as the codes
-        const float f = e >= 255 ? NAN : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            sq[nt][j] = __shfl_sync(0xffffffffu, sum, (2 * t4 + j) * 4);
-            rf[nt][j] = __shfl_sync(0xffffffffu, f, (2 * t4 + j) * 4);
-            const int r = nt * 8 + 2 * t4 + j;
-            const int qp = qpos0 + (r0 + r) / p.G;
-            hi[nt][j] = p.causal ? min(nk, qp + 1) : nk;
-            lo[nt][j] = p.window > 0 ? max(0, qp - p.window + 1) : 0;
-        }
-    }
-    const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
-
-    float oacc[D / 16][NT][4];
-    float mu[NT][2], l[NT][2], za[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) oacc[m][nt][e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            mu[nt][j] = kNegInf;
-            l[nt][j] = 0.f;
-            za[nt][j] = 0.f;
-        }
-    }
-    uint32_t ev = 14;                   // biased exponent of the largest V scale so far
     float2* sck = reinterpret_cast<float2*>(smem + C::OFF_SCALES + warp * C::SCALES);
     float2* scv = sck + C::BN;
+    float4* stats = reinterpret_cast<float4*>(smem + C::OFF_STATS);     // [WARPS][ROWS] max, sum, factor
+    uint32_t stage = 0, phase = 0;      // ring position over all segments
+    bool ok = true;
 
-    for (int i = 0; i < ntile; ++i) {
-        if (i + C::NSTAGE - 1 < ntile)
-            load_tile(first + (i + C::NSTAGE - 1) * C::WARPS, (i + C::NSTAGE - 1) % C::NSTAGE);
-        cp_async_commit();
-        cp_async_wait<C::NSTAGE - 1>();
-        __syncwarp();
-        const uint8_t* st = ring + (i % C::NSTAGE) * C::STAGE;
-        const int k0 = (first + i * C::WARPS) * C::BN;
-
-        // ---- scales and zeros: lane = key
-        float dscale;                   // 2^(old - new) exponent of the V scaling
-        {
-            const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + 2 * C::TILE);
-            uint32_t wk = ws[lane], wv = ws[C::BN + lane];
-            if (wv >= 0x7f80u) {        // a row that holds NaN or infinity: it acts through its score
-                wk = kKv4NaN;
-                wv = 0;
-            }
-            const uint32_t e_new = max(ev, __reduce_max_sync(0xffffffffu, wv >> 7));
-            dscale = __uint_as_float((127u - min(e_new - ev, 127u)) << 23);
-            ev = e_new;
-            const float vs = __uint_as_float((wv & 0xfff0u) << 16) * __uint_as_float((268u - ev) << 23);
-            sck[lane] = make_float2(__uint_as_float((wk & 0xfff0u) << 16),
-                                    __uint_as_float(0x4b000000u | (wk & 15u)) - 8388608.f);
-            scv[lane] = make_float2(vs, __uint_as_float(0x4b000000u | (wv & 15u)) - 8388608.f);
+    while (x < x_end) {
+        // ------------------------------------------------- a segment --
+        const Kv4Span sp = kv4_span<C::BN>(p, b);
+        if (sp.n == 0) {
+            ++b;
+            continue;
         }
-        __syncwarp();
+        const int item = static_cast<int>((x - base) / sp.n);
+        const int tile0 = static_cast<int>((x - base) - static_cast<int64_t>(item) * sp.n);
+        const int count = static_cast<int>(min(static_cast<int64_t>(sp.n - tile0), x_end - x));
+        const int hk = item / p.row_blocks;
+        const int r0 = (item - hk * p.row_blocks) * C::ROWS;     // first of the query rows
+        const int nrows = min(C::ROWS, p.Nq * p.G - r0);
+        const int nk = sp.nk, qpos0 = nk - p.Nq;                 // key position of query 0
 
-        // ---- S^T = C^k q^T: 32 keys x 8 NT rows
-        float s[2][NT][4];
+        const int64_t head = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk;
+        const int first = sp.t0 + tile0 + warp;
+        const int ntile = ok && warp < count ? (count - warp + C::WARPS - 1) / C::WARPS : 0;
+        // what the warp's next load reads
+        int64_t row_next = head + static_cast<int64_t>(first) * C::BN;
+        int room_next = p.Nk - first * C::BN;
+        auto load_next = [&](int slot) {
+            if (lane == 0) {
+                const uint32_t rows = min(C::BN, room_next);     // a multiple of 8
+                uint8_t* dst = ring + slot * C::STAGE;
+                mbar_arrive_expect_tx(bars + slot, rows * (2 * C::ROWB + 4));
+                bulk_load(dst, p.codes[0] + row_next * C::ROWB, rows * C::ROWB, bars + slot);
+                bulk_load(dst + C::TILE, p.codes[1] + row_next * C::ROWB, rows * C::ROWB, bars + slot);
+                bulk_load(dst + 2 * C::TILE, p.words[0] + row_next, rows * 2, bars + slot);
+                bulk_load(dst + 2 * C::TILE + C::WORDB, p.words[1] + row_next, rows * 2, bars + slot);
+            }
+            row_next += C::WARPS * C::BN;
+            room_next -= C::WARPS * C::BN;
+        };
+        {
+            int slot = stage;
+            for (int i = 0; i < min(C::NSTAGE, ntile); ++i) {
+                load_next(slot);
+                slot = slot + 1 == C::NSTAGE ? 0 : slot + 1;
+            }
+        }
+
+        // ------------------------------------- queries as B fragments --
+        // Row nt * 8 + g8, channels t4 * D/4 ..: of word w (8 codes), pair u of
+        // k-step pairs: codes (2u, 2u + 4) plain and (2u + 1, 2u + 5) times 1/16.
+        constexpr int W = D / 32;
+        uint32_t qf[NT][W][2][2];
+        float2 sq[NT], rf[NT];          // of rows nt * 8 + 2 t4 + {0, 1}: sum of q and the score factor
+        int hi[NT][2], lo[NT][2];       // their allowed keys are [lo, hi)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int nt = 0; nt < NT; ++nt) {
+            const int rr = nt * 8 + g8;
+            uint4 raw[W];
+            const bool have = rr < nrows;
+            const int qi = (r0 + rr) / p.G;
+            const size_t qrow = have ? (static_cast<size_t>(b) * p.Nq + qi) * p.H + hk * p.G + (r0 + rr) - qi * p.G : 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                raw[w] = have ? *reinterpret_cast<const uint4*>(p.q + qrow * D + t4 * (D / 4) + w * 8) : make_uint4(0, 0, 0, 0);
+            uint32_t top = 0;           // largest magnitude, as bf16 bits (NaN and infinity on top)
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, (v[j] >> 16) & 0x7fffu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max(static_cast<int>(top >> 7), 14);             // biased exponent
+            const float qs = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f[8] = {bf16_lo(raw[w].x) * qs, bf16_hi(raw[w].x) * qs, bf16_lo(raw[w].y) * qs,
+                                    bf16_hi(raw[w].y) * qs, bf16_lo(raw[w].z) * qs, bf16_hi(raw[w].z) * qs,
+                                    bf16_lo(raw[w].w) * qs, bf16_hi(raw[w].w) * qs};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += f[j];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    qf[nt][w][u][0] = pack_f16(f[2 * u], f[2 * u + 4]);
+                    qf[nt][w][u][1] = pack_f16(f[2 * u + 1] * 0.0625f, f[2 * u + 5] * 0.0625f);
+                }
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sum *= -5.9604644775390625e-8f;                                // -2^-24, as the codes
+            const float f = e >= 255 ? NAN : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
+            sq[nt].x = __shfl_sync(0xffffffffu, sum, 8 * t4);
+            sq[nt].y = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+            rf[nt].x = __shfl_sync(0xffffffffu, f, 8 * t4);
+            rf[nt].y = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int qp = qpos0 + (r0 + nt * 8 + 2 * t4 + j) / p.G;
+                hi[nt][j] = p.causal ? min(nk, qp + 1) : nk;
+                lo[nt][j] = p.window > 0 ? max(0, qp - p.window + 1) : 0;
+            }
+        }
+        const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
+
+        float2 oacc[D / 16][NT][2];     // [m][nt][row g8 / g8 + 8 of the mma], rows 2 t4 + {0, 1}
+        float2 l[NT], za[NT], nm[NT];   // sums of p and of p s^v z, minus the reference (kNoRef: none yet)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) oacc[m][nt][0] = oacc[m][nt][1] = make_float2(0.f, 0.f);
+            l[nt] = za[nt] = make_float2(0.f, 0.f);
+            nm[nt] = make_float2(kNoRef, kNoRef);
+        }
+        uint32_t ev = 6;                // biased exponent of the largest V scale so far
+        float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
+
+        for (int i = 0; i < ntile; ++i) {
+            if (!__all_sync(0xffffffffu, mbar_wait(bars + stage, phase, wc))) { ok = false; break; }
+            const uint8_t* st = ring + stage * C::STAGE;
+            const int k0 = (first + i * C::WARPS) * C::BN;
+
+            // ---- scales and zeros: a key a lane
+            const bool edge = k0 + C::BN > nk;
+            {
+                const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + 2 * C::TILE);
+                uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
+#pragma unroll
+                for (int kk = 0; kk < C::BN / 32; ++kk) {
+                    wk[kk] = ws[kk * 32 + lane];
+                    wv[kk] = ws[C::BN + kk * 32 + lane];
+                    top = max(top, wv[kk]);
+                }
+                top = __reduce_max_sync(0xffffffffu, top) >> 7;
+                if (edge || top >= 255u) {
+                    // rows past the sequence may hold anything; a row whose V is
+                    // NaN acts through its score
+                    top = 0;
+#pragma unroll
+                    for (int kk = 0; kk < C::BN / 32; ++kk) {
+                        if (wv[kk] >= 0x7f80u) {
+                            wk[kk] = kKv4NaN;
+                            wv[kk] = 0;
+                        }
+                        if (k0 + kk * 32 + lane >= nk) wv[kk] = 0;
+                        top = max(top, wv[kk]);
+                    }
+                    top = __reduce_max_sync(0xffffffffu, top) >> 7;
+                }
+                if (top > ev) {         // a larger scale than any before: O goes down with the new factor
+                    const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        za[nt] = fmul2(za[nt], make_float2(d, d));
+#pragma unroll
+                        for (int m = 0; m < D / 16; ++m) {
+                            oacc[m][nt][0] = fmul2(oacc[m][nt][0], make_float2(d, d));
+                            oacc[m][nt][1] = fmul2(oacc[m][nt][1], make_float2(d, d));
+                        }
+                    }
+                    ev = top;
+                    vnorm = __uint_as_float((260u - ev) << 23);
+                }
+#pragma unroll
+                for (int kk = 0; kk < C::BN / 32; ++kk) {
+                    sck[kk * 32 + lane] = make_float2(__uint_as_float((wk[kk] & 0xfff0u) << 16),
+                                                      __uint_as_float(0x4b000000u | (wk[kk] & 15u)) - 8388608.f);
+                    scv[kk * 32 + lane] = make_float2(__uint_as_float((wv[kk] & 0xfff0u) << 16) * vnorm,
+                                                      __uint_as_float(0x4b000000u | (wv[kk] & 15u)) - 8388608.f);
+                }
+            }
+            __syncwarp();
+
+            // ---- S^T = C^k q^T: keys x 8 NT rows
+            float2 s[C::MT][NT][2];
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m) {
+                uint32_t ka[W], kb[W];
+                const uint8_t* ra = st + (m * 16 + kv4_key(g8)) * C::ROWB + t4 * (W * 4);
+                const uint8_t* rb = ra + 8 * C::ROWB;
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
+                    ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+                    kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(rb);
+                    ka[0] = u.x; ka[1] = u.y;
+                    kb[0] = v.x; kb[1] = v.y;
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t u = ka[w], v = kb[w], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (w == 0)
+                            mma_f16_first(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                          qf[nt][w][0][1]);
+                        else
+                            mma_f16(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                    qf[nt][w][0][1]);
+                        mma_f16(s[m][nt], u8 & kNibLo, v8 & kNibLo, u8 & kNibHi, v8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
+                    }
+                }
+            }
+            // ---- scores (over the row factor rf) and masks
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 sz = sck[m * 16 + half * 8 + kv4_key(g8)];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
+                                               make_float2(sz.x, sz.x));
+                }
+            if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int key = k0 + m * 16 + half * 8 + kv4_key(g8);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
+                            if (key >= hi[nt][1] || key < lo[nt][1]) s[m][nt][half].y = kNegInf;
+                        }
+                    }
+            }
+            // ---- p = 2^(x - reference).  A lane's sum over the tile tells when a
+            // score has passed the reference by so much that p s^v could leave
+            // fp16: then the reference moves to the maximum and p is taken anew.
+            float2 e[C::MT][NT][2], ts[NT];
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                ts[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
+                        e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
+                        ts[nt] = fadd2(ts[nt], e[m][nt][half]);
+                    }
+                over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
+            }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float2 mx = s[0][nt][0];
+#pragma unroll
+                    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            mx.x = fmaxf(mx.x, s[m][nt][half].x);
+                            mx.y = fmaxf(mx.y, s[m][nt][half].y);
+                        }
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+                        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+                    }
+                    // the reference never falls; -inf (nothing yet) leaves none
+                    float2 n2 = fmul2(mx, make_float2(-rf[nt].x, -rf[nt].y));
+                    n2 = make_float2(fminf(n2.x, nm[nt].x), fminf(n2.y, nm[nt].y));
+                    const float2 a = make_float2(nm[nt].x == kNoRef ? 0.f : ex2(n2.x - nm[nt].x),
+                                                 nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
+                    nm[nt] = n2;
+                    l[nt] = fmul2(l[nt], a);
+                    za[nt] = fmul2(za[nt], a);
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
+                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
+                    }
+                    ts[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
+                            e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
+                            ts[nt] = fadd2(ts[nt], e[m][nt][half]);
+                        }
+                }
+            }
+            // ---- p s^v as the B fragments of the second product
+            uint32_t pf[C::MT][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) l[nt] = fadd2(l[nt], ts[nt]);
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 sz = scv[m * 16 + half * 8 + kv4_key(g8)];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 w = fmul2(e[m][nt][half], make_float2(sz.x, sz.x));
+                        za[nt] = ffma2(w, make_float2(sz.y, sz.y), za[nt]);
+                        pf[m][nt][half] = transpose8x8(pack_f16(w.x, w.y));
+                    }
+                }
+            // ---- O^T += C^v (p s^v)^T
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m) {
+                constexpr int VW = D / 64;                 // words of codes a lane and key
+                uint32_t v[4][VW];                         // mma indices 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int row = m * 16 + (kk >> 1) * 8 + kv4_key(2 * t4 + (kk & 1));
+                    const uint8_t* src = st + C::TILE + row * C::ROWB + g8 * (VW * 4);
+                    if constexpr (D == 128) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(src);
+                        v[kk][0] = u.x;
+                        v[kk][VW - 1] = u.y;
+                    } else {
+                        v[kk][0] = *reinterpret_cast<const uint32_t*>(src);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w)
+#pragma unroll
+                    for (int up = 0; up < 2; ++up) {       // codes 0-3, then 4-7 of the word
+                        const uint32_t sel = up ? 0x7632u : 0x5410u;
+                        const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
+                        const uint32_t u8 = u >> 8, y8 = y >> 8;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(oacc[w * 4 + up * 2][nt], u & kNibLo, u & kNibHi, y & kNibLo, y & kNibHi,
+                                    pf[m][nt][0], pf[m][nt][1]);
+                            mma_f16(oacc[w * 4 + up * 2 + 1][nt], u8 & kNibLo, u8 & kNibHi, y8 & kNibLo, y8 & kNibHi,
+                                    pf[m][nt][0], pf[m][nt][1]);
+                        }
+                    }
+            }
+            __syncwarp();               // the stage may be loaded again
+            if (i + C::NSTAGE < ntile) load_next(stage);
+            stage = stage + 1 == C::NSTAGE ? 0 : stage + 1;
+            phase ^= stage == 0;
+        }
+
+        // ------------------------------------------- merge of the warps --
+        const float back = ldexpf(1.f, static_cast<int>(ev) - 133);       // undoes vnorm
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+                l[nt].x += __shfl_xor_sync(0xffffffffu, l[nt].x, o);
+                l[nt].y += __shfl_xor_sync(0xffffffffu, l[nt].y, o);
+                za[nt].x += __shfl_xor_sync(0xffffffffu, za[nt].x, o);
+                za[nt].y += __shfl_xor_sync(0xffffffffu, za[nt].y, o);
+            }
+            if (g8 == 0) {
+                float4* d = stats + warp * C::ROWS + nt * 8 + 2 * t4;
+                d[0] = make_float4(nm[nt].x == kNoRef ? kNegInf : -nm[nt].x, l[nt].x, back, 0.f);
+                d[1] = make_float4(nm[nt].y == kNoRef ? kNegInf : -nm[nt].y, l[nt].y, back, 0.f);
+            }
+        }
+        if (ntile > 0) {
+            // channel g8 * D/8 + n at n * 8 + g8: neighbouring lanes, neighbouring banks
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[m][nt][e] = 0.f;
-            uint32_t ka[W], kb[W];
-            const uint8_t* ra = st + (m * 16 + g8) * C::ROWB + t4 * (W * 4);
-            const uint8_t* rbp = ra + 8 * C::ROWB;
-            if constexpr (D == 128) {
-                const uint4 a = *reinterpret_cast<const uint4*>(ra), bb = *reinterpret_cast<const uint4*>(rbp);
-                ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
-                kb[0] = bb.x; kb[1] = bb.y; kb[2] = bb.z; kb[3] = bb.w;
+                for (int m = 0; m < D / 16; ++m) {
+                    float* d0 = reinterpret_cast<float*>(ring) + (nt * 8 + 2 * t4) * C::OSTRIDE + g8 + 16 * m;
+                    float* d1 = d0 + C::OSTRIDE;
+                    d0[0] = fmaf(oacc[m][nt][0].x, 16777216.f, -za[nt].x);         // codes times 2^-24
+                    d1[0] = fmaf(oacc[m][nt][0].y, 16777216.f, -za[nt].y);
+                    d0[8] = fmaf(oacc[m][nt][1].x, 1048576.f, -za[nt].x);          // and 2^-20
+                    d1[8] = fmaf(oacc[m][nt][1].y, 1048576.f, -za[nt].y);
+                }
+        }
+        __syncthreads();
+        const bool whole = count == sp.n;
+        for (int r = warp; r < nrows; r += C::WARPS) {
+            const float4 mine = lane < C::WARPS ? stats[lane * C::ROWS + r] : make_float4(kNegInf, 0.f, 0.f, 0.f);
+            float M = mine.x;
+#pragma unroll
+            for (int o = C::WARPS / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float f = mine.x == kNegInf && !isnan(mine.y) ? 0.f : ex2(mine.x - M);
+            float L = f * mine.y;
+#pragma unroll
+            for (int o = C::WARPS / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            const float fb = f * mine.z;
+            M = __shfl_sync(0xffffffffu, M, 0);
+            L = __shfl_sync(0xffffffffu, L, 0);
+            float a[D / 32];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w) {
+                const float fw = __shfl_sync(0xffffffffu, fb, w);
+                if (fw == 0.f) continue;        // nothing there (NaN goes on)
+                const float* src = reinterpret_cast<const float*>(smem + w * C::RING) + r * C::OSTRIDE + lane * (D / 32);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) a[e] = fmaf(src[e], fw, a[e]);
+            }
+            if (whole) {
+                kv4_store_row<D>(p, b, hk, r0 + r, a, M, L);
             } else {
-                const uint2 a = *reinterpret_cast<const uint2*>(ra), bb = *reinterpret_cast<const uint2*>(rbp);
-                ka[0] = a.x; ka[1] = a.y;
-                kb[0] = bb.x; kb[1] = bb.y;
-            }
+                const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (tile0 == 0)) * C::ROWS + r;
+                float* dst = p.o_part + at * D + lane * (D / 32);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const uint32_t x = ka[w], y = kb[w], x8 = x >> 8, y8 = y >> 8;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(s[m][nt], x & kNibLo, y & kNibLo, x & kNibHi, y & kNibHi, qf[nt][w][0][0], qf[nt][w][0][1]);
-                    mma_f16(s[m][nt], x8 & kNibLo, y8 & kNibLo, x8 & kNibHi, y8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
-                }
+                for (int e = 0; e < D / 32; ++e) dst[e] = a[e];
+                if (lane == 0) p.ml_part[at] = make_float2(M, L);
             }
         }
-        // ---- scores (over the row factor rf) and masks
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float2 sz = sck[m * 16 + half * 8 + g8];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        s[m][nt][half * 2 + j] = fmaf(-sz.y, sq[nt][j], s[m][nt][half * 2 + j]) * sz.x;
-            }
-        if (k0 + C::BN > nk || (p.causal && k0 + C::BN - 1 > qp_first) ||
-            (p.window > 0 && k0 <= qp_last - p.window)) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = k0 + m * 16 + (e >> 1) * 8 + g8;
-                        if (key >= hi[nt][e & 1] || key < lo[nt][e & 1]) s[m][nt][e] = kNegInf;
-                    }
+        x += count;
+        if (x - base == static_cast<int64_t>(sp.n) * per) {
+            base = x;
+            ++b;
         }
-        // ---- running maximum
-        float alpha[NT][2];
-        bool change = dscale != 1.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float mx = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                alpha[nt][j] = 1.f;
-                if (mx > mu[nt][j]) {
-                    alpha[nt][j] = ex2((mu[nt][j] - mx) * rf[nt][j]);     // 0 from -inf
-                    mu[nt][j] = mx;
-                    change = true;
-                }
-            }
-        if (__any_sync(0xffffffffu, change)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    l[nt][j] *= alpha[nt][j];
-                    alpha[nt][j] *= dscale;
-                    za[nt][j] *= alpha[nt][j];
-                }
-#pragma unroll
-                for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) oacc[m][nt][e] *= alpha[nt][e & 1];
-            }
-        }
-        // ---- p, and p s^v as the B fragments of the second product
-        uint32_t pf[2][NT][2];
-        float nm[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) nm[nt][j] = mu[nt][j] == kNegInf ? 0.f : -mu[nt][j] * rf[nt][j];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float2 sz = scv[m * 16 + half * 8 + g8];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float e = ex2(fmaf(s[m][nt][half * 2 + j], rf[nt][j], nm[nt][j]));
-                        l[nt][j] += e;
-                        w[j] = e * sz.x;
-                        za[nt][j] = fmaf(w[j], sz.y, za[nt][j]);
-                    }
-                    pf[m][nt][half] = transpose8x8(pack_f16(w[0], w[1]));
-                }
-            }
-        // ---- O^T += C^v (p s^v)^T
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            constexpr int VW = D / 64;                     // words of codes a lane and key
-            uint32_t v[4][VW];                             // keys 2t, 2t+1, 2t+8, 2t+9
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int row = m * 16 + (kk >> 1) * 8 + (kk & 1) * 4 + t4;     // kv4_v_row
-                if constexpr (D == 128) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(
-                        st + C::TILE + row * C::ROWB + kv4_v_chunk<D>(row, g8 >> 1) * 16 + (g8 & 1) * 8);
-                    v[kk][0] = x.x;
-                    v[kk][VW - 1] = x.y;
-                } else {
-                    v[kk][0] = *reinterpret_cast<const uint32_t*>(st + C::TILE + row * C::ROWB + g8 * 4);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-#pragma unroll
-                for (int up = 0; up < 2; ++up) {           // codes 0-3, then 4-7 of the word
-                    const uint32_t sel = up ? 0x7632u : 0x5410u;
-                    const uint32_t x = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(oacc[w * 4 + up * 2][nt], x & kNibLo, x & kNibHi, y & kNibLo, y & kNibHi,
-                                pf[m][nt][0], pf[m][nt][1]);
-                        mma_f16(oacc[w * 4 + up * 2 + 1][nt], x8 & kNibLo, x8 & kNibHi, y8 & kNibLo, y8 & kNibHi,
-                                pf[m][nt][0], pf[m][nt][1]);
-                    }
-                }
-        }
-        __syncwarp();                   // the stage may be loaded again
+        fence_proxy_async_smem();       // the ring's next contents come by bulk copy
+        __syncthreads();
     }
+    if (!ok && lane == 0) {
+        // let the copies in flight land before the CTA exits
+        volatile int no_abort = 0;
+        const WaitCtl dw{&no_abort, p.error_word, 200000000ull};
+        for (int s = 0; s < C::NSTAGE; ++s) {
+            mbar_wait(bars + stage, phase, dw);
+            stage = stage + 1 == C::NSTAGE ? 0 : stage + 1;
+            phase ^= stage == 0;
+        }
+    }
+}
 
-    // -------------------------------------------------- merge of the warps --
-    cp_async_wait<0>();
-    float* sm_m = reinterpret_cast<float*>(smem + C::OFF_STATS);       // [WARPS][ROWS], base 2
-    float* sm_l = sm_m + C::WARPS * C::ROWS;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
-                za[nt][j] += __shfl_xor_sync(0xffffffffu, za[nt][j], o);
-            }
-            mu[nt][j] = mu[nt][j] == kNegInf ? kNegInf : mu[nt][j] * rf[nt][j];
-            if (g8 == 0) {
-                sm_m[warp * C::ROWS + nt * 8 + 2 * t4 + j] = mu[nt][j];
-                sm_l[warp * C::ROWS + nt * 8 + 2 * t4 + j] = l[nt][j];
-            }
-        }
-    __syncthreads();                    // also: every warp is done with its ring
-    float* so = reinterpret_cast<float*>(smem);            // [WARPS][ROWS][OSTRIDE]
-    const float back = ldexpf(1.f, static_cast<int>(ev) - 141);       // undoes 2^(14 - (ev - 127))
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = nt * 8 + 2 * t4 + j;
-            float M = kNegInf;
-#pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, sm_m[w * C::ROWS + r]);
-            const float f = mu[nt][j] == kNegInf && !isnan(l[nt][j]) ? 0.f : ex2(mu[nt][j] - M) * back;
-            float* dst = so + (warp * C::ROWS + r) * C::OSTRIDE + g8;
-            // channel g8 * D/8 + n sits at n * 8 + g8: eight lanes, eight banks
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) {
-                dst[(2 * m) * 8] = fmaf(oacc[m][nt][j], 16777216.f, -za[nt][j]) * f;       // 2^24
-                dst[(2 * m + 1) * 8] = fmaf(oacc[m][nt][2 + j], 1048576.f, -za[nt][j]) * f;    // 2^20
-            }
-        }
-    __syncthreads();
-    for (int e = threadIdx.x; e < nrows * (D / 2); e += C::WARPS * 32) {
-        const int r = e / (D / 2), c2 = (e % (D / 2)) * 2;
-        const int at = (c2 % (D / 8)) * 8 + c2 / (D / 8);
-        float M = kNegInf, L = 0.f, a0 = 0.f, a1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, sm_m[w * C::ROWS + r]);
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-            const float mw = sm_m[w * C::ROWS + r], lw = sm_l[w * C::ROWS + r];
-            L += mw == kNegInf && !isnan(lw) ? 0.f : lw * ex2(mw - M);
-            a0 += so[(w * C::ROWS + r) * C::OSTRIDE + at];
-            a1 += so[(w * C::ROWS + r) * C::OSTRIDE + at + 8];
-        }
-        const bool some = !(L == 0.f);              // NaN stays NaN
-        const float inv = some ? 1.f / L : 0.f;
-        const float lse2 = some ? M + __log2f(L) : kNegInf;
-        const int i = (r0 + r) / p.G, h = hk * p.G + (r0 + r) % p.G;
-        const size_t row = static_cast<size_t>(b) * p.Nq + i;
-        if (p.nsplit == 1) {
-            *reinterpret_cast<uint32_t*>(p.o + (row * p.H + h) * D + c2) = pack_bf16(a0 * inv, a1 * inv);
-            if (c2 == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = lse2 * 0.6931471805599453f;
-        } else {
-            *reinterpret_cast<float2*>(p.o_part + ((static_cast<size_t>(split) * rows_q + row) * p.H + h) * D + c2) =
-                make_float2(a0 * inv, a1 * inv);
-            if (c2 == 0) p.lse_part[(static_cast<size_t>(split) * p.H + h) * rows_q + row] = lse2;
-        }
+// Merges the partial results of the items that lie in several ranges, and
+// writes the outputs of sequences without keys.  A CTA to a query row; its
+// warps take every fourth range.
+template <int D, int NT>
+__global__ void __launch_bounds__(128)
+kv4_merge_kernel(const Kv4DecodeParams p) {
+    using C = Kv4DecCfg<D, NT>;
+    constexpr int V = D / 32;
+    __shared__ float sm_a[4][D];
+    __shared__ float2 sm_ml[4];
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    const int per = p.Hkv * p.row_blocks;
+    const int rows = p.Nq * p.G;
+    const int r = blockIdx.x % rows, bh = blockIdx.x / rows;
+    const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+    const int item = hk * p.row_blocks + r / C::ROWS;
+    int64_t total = 0, at = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int n = kv4_span<C::BN>(p, i).n;
+        total += n;
+        if (i < b) at += n;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        at += __shfl_xor_sync(0xffffffffu, at, o);
+    }
+    const int n = kv4_span<C::BN>(p, b).n;
+    total *= per;
+    at = at * per + static_cast<int64_t>(item) * n;
+    const int ranges = kv4_ranges<C::WARPS>(p, total);
+    auto range_of = [&](int64_t x) {            // the range that holds tile x
+        int c = static_cast<int>(x * ranges / total);
+        while (total * (c + 1) / ranges <= x) ++c;
+        while (total * c / ranges > x) --c;
+        return c;
+    };
+    const int c0 = n > 0 ? range_of(at) : 0, c1 = n > 0 ? range_of(at + n - 1) : 0;
+    // launched as a programmatic dependent of the kernel above: from here on
+    // its results are complete.  Every thread waits, so that this grid does not
+    // end before that one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float a[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] = 0.f;
+    if (n == 0) {
+        if (warp == 0) kv4_store_row<D>(p, b, hk, r, a, -INFINITY, 0.f);
+        return;
+    }
+    if (c0 == c1) return;                       // written by the range's own CTA
+    auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0)) * C::ROWS + r % C::ROWS; };
+    float M = -INFINITY, L = 0.f;
+    auto take = [&](float m, float sum, const float (&v)[V]) {
+        if (m == -INFINITY && !isnan(sum)) return;      // no key of this row
+        const float m_new = fmaxf(M, m);
+        const float w0 = M == -INFINITY ? 0.f : ex2(M - m_new), w1 = ex2(m - m_new);
+        L = (M == -INFINITY ? L : L * w0) + sum * w1;
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[e] = fmaf(v[e], w1, a[e] * w0);
+        M = m_new;
+    };
+    for (int c = c0 + warp; c <= c1; c += 16) {
+        float v[4][V];
+        float2 ml[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at_slot = slot(min(c + 4 * i, c1));
+            ml[i] = c + 4 * i <= c1 ? p.ml_part[at_slot] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] = p.o_part[at_slot * D + lane * V + e];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take(ml[i].x, ml[i].y, v[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sm_a[warp][lane * V + e] = a[e];
+    if (lane == 0) sm_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = sm_a[w][lane * V + e];
+        take(sm_ml[w].x, sm_ml[w].y, v);
+    }
+    kv4_store_row<D>(p, b, hk, r, a, M, L);
 }
 
 }  // namespace fa

@@ -55,6 +55,7 @@ def attend_args(**kw):
     (dict(causal=0, window=8), -5),
     (dict(num_splits=2), -6), (dict(num_splits=2, workspace=P, workspace_bytes=100), -6),
     (dict(Nq=100), -6), (dict(Nq=100, workspace=P, workspace_bytes=1000), -6),
+    (dict(num_splits=0, Nk=65536), -6),
     (dict(scale=0.0), -9), (dict(scale=float("nan")), -9),
     (dict(Nq=0), 0), (dict(B=0), 0),
 ])
@@ -63,19 +64,23 @@ def test_attention_validation(kw, code):
 
 
 def test_sizes():
-    # one split and few rows need nothing; splits need their partials; a chunk
-    # needs the bf16 rows as well
-    assert fa.fa_fwd_kv4_workspace_size(2, 8, 2, 1, 512, 128, 1) == 0
-    assert fa.fa_fwd_kv4_workspace_size(2, 8, 2, 1, 512, 128, 4) == 4 * 2 * 8 * 129 * 4 // 256 * 256 + 256 * (
-        4 * 2 * 8 * 129 * 4 % 256 != 0)
-    chunk = fa.fa_fwd_kv4_workspace_size(2, 8, 2, 500, 512, 128, 1)
-    assert chunk == 2 * (2 * 512 * 2 * 128 * 2)
-    assert fa.fa_fwd_kv4_workspace_size(2, 8, 3, 1, 512, 128, 4) == 0       # 8 heads over 3: refused
-    for shape in [(1, 8, 2, 1, 8, 128), (16, 16, 16, 1, 8192, 128), (1, 32, 8, 1, 131072, 128),
-                  (4, 16, 16, 2048, 8192, 128), (1, 8, 1, 16, 40, 64)]:
-        assert 1 <= fa.fa_fwd_kv4_num_splits(*shape) <= 32
-    assert fa.fa_fwd_kv4_num_splits(0, 8, 2, 1, 8, 128) == 1
-    assert fa.fa_fwd_kv4_num_splits(1, 8, 3, 1, 8, 128) == 1
+    # one split and few rows need nothing; ranges need two partial results of
+    # 8 or 16 rows (d values, maximum, sum) each; a chunk needs its splits'
+    # partials and the bf16 rows
+    def up(n):
+        return (n + 255) // 256 * 256
+
+    size = fa.fa_fwd_kv4_workspace_size
+    assert size(2, 8, 2, 1, 512, 128, 1) == 0
+    assert size(2, 8, 2, 1, 512, 128, 4) == up(2 * (4 * 2 * 2) * 8 * 130 * 4)
+    assert size(2, 8, 2, 3, 512, 64, 4) == up(2 * (4 * 2 * 2) * 16 * 66 * 4)
+    assert size(2, 8, 2, 7, 512, 64, 3) == up(2 * (3 * 2 * 2 * 2) * 16 * 66 * 4)
+    back = 2 * (2 * 512 * 2 * 128 * 2)
+    assert size(2, 8, 2, 500, 512, 128, 1) == back
+    assert size(2, 8, 2, 500, 512, 128, 3) == back + up(3 * 2 * 500 * 8 * 129 * 4)
+    assert size(2, 8, 2, 1, 512, 128, 0) >= 0 and size(2, 8, 2, 500, 512, 128, 0) >= back
+    assert size(2, 8, 3, 1, 512, 128, 4) == 0       # 8 heads over 3: refused
+    assert size(0, 8, 2, 1, 512, 128, 4) == 0 and size(2, 8, 2, 1, 512, 128, -1) == 0
 
 
 # ------------------------------------------------------------- the binding --
