@@ -230,13 +230,13 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  *   Up to 32 query rows to a key/value head (Nq * H / Hkv) run on a kernel
  * that multiplies the 4-bit codes as they are; more are run by reading the
  * rows in use back into the workspace for the tensor-core forward.
- *   num_splits : few rows: 1 gives every (sequence, key/value head) one CTA,
- * more cut the keys of all of them together into num_splits equal ranges to
- * each; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.
+ *   num_splits : few rows: the keys of all sequences and heads together are
+ * cut into equal ranges, num_splits to each (sequence, key/value head) on
+ * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.
  *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
- * bytes (of the current device, for num_splits = 0), 16-byte aligned (0 bytes,
- * and NULL allowed, for few rows and one split); contents on entry do not
- * matter.  Calls that may overlap on the GPU need one each.
+ * bytes (for num_splits = 0 they are those of the current device), 16-byte
+ * aligned; contents on entry do not matter.  Calls that may overlap on the GPU
+ * need one each.
  * Errors as fa_fwd_kvcache; H not a multiple of Hkv is FA_ERR_BAD_SHAPE.
  */
 int fa_quantize_kv4(const void* k, const void* v, void* k_codes, void* k_words, void* v_codes,

@@ -458,14 +458,12 @@ int64_t kv4_row_blocks(int64_t rows) {
     return (rows + per - 1) / per;
 }
 
-// Ranges that kv4_decode_kernel cuts its work into (0: a CTA to each item and
-// no merge).
-int kv4_range_count(int B, int Hkv, int Nq, int group, int Nk, int num_splits, int num_sms) {
-    const int64_t rows = static_cast<int64_t>(Nq) * group;
-    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
-    if (num_splits == 1 || Nk == 0) return 0;
-    if (num_splits > 1) return static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20));
-    return 3 * num_sms;
+// Ranges that kv4_decode_kernel cuts its work into: the warps that run at once
+// on all SMs (12 an SM), or num_splits to an item.
+int kv4_range_count(int B, int Hkv, int Nq, int group, int num_splits, int num_sms) {
+    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(static_cast<int64_t>(Nq) * group);
+    if (num_splits > 0) return static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20));
+    return 12 * num_sms;
 }
 
 int current_sms() {
@@ -487,7 +485,7 @@ size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int num_spli
     const int group = H / Hkv;
     if (!kv4_direct(Nq, group, Nk))
         return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
-    const size_t rows = 2 * static_cast<size_t>(kv4_range_count(B, Hkv, Nq, group, Nk, num_splits, num_sms)) *
+    const size_t rows = 2 * static_cast<size_t>(kv4_range_count(B, Hkv, Nq, group, num_splits, num_sms)) *
                         kv4_block_rows(static_cast<int64_t>(Nq) * group);
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
@@ -571,17 +569,18 @@ int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_wo
 template <int D, int NT>
 int launch_kv4_decode(const fa::Kv4DecodeParams& p, cudaStream_t stream) {
     using C = fa::Kv4DecCfg<D, NT>;
-    const int items = p.B * p.Hkv * p.row_blocks;
+    const int grid = (p.ranges + C::WARPS - 1) / C::WARPS;
     const int slot = prof_start(4, stream);
-    fa::kv4_decode_kernel<D, NT><<<p.ranges > 0 ? p.ranges : items, C::WARPS * 32, C::SMEM, stream>>>(p);
+    fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(p);
     prof_stop(4, slot, stream);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    if (p.ranges == 0) return FA_OK;
     const int slot2 = prof_start(5, stream);
     // programmatic dependent launch, as the merge of the bf16 decode
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Nq * p.H));
-    cfg.blockDim = dim3(128);
+    // as many warps as bring an item's partials in with one or two waits
+    const int items = p.B * p.Hkv * p.row_blocks;
+    cfg.blockDim = dim3(p.ranges / items >= 32 ? 32 * fa::kKv4MergeWarps : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -915,7 +914,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.window = window > 0 ? window : 0;
     const int64_t rows = static_cast<int64_t>(Nq) * group;
     p.row_blocks = static_cast<int>(kv4_row_blocks(rows));
-    p.ranges = kv4_range_count(B, Hkv, Nq, group, Nk, num_splits, st->num_sms);
+    p.ranges = kv4_range_count(B, Hkv, Nq, group, num_splits, st->num_sms);
     p.o_part = part;
     p.ml_part = reinterpret_cast<float2*>(part + 2 * static_cast<size_t>(p.ranges) * kv4_block_rows(rows) * d);
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -28,11 +28,10 @@
 // memory as 16-bit words first, four times the cache's bytes.
 //
 // The key tiles of all heads and sequences are cut into equal ranges, one a
-// CTA (kv4_span below).  In a range one warp is on its own: it takes every
-// WARPS-th tile of 32 keys through its own ring of bulk copies, with its own
-// running maximum and sums, so the key loop has no CTA barrier; the warps'
-// results merge at the end of an item, those of an item that lies in several
-// ranges in kv4_merge_kernel.
+// warp (kv4_span below).  A warp is on its own: it takes its tiles through its
+// own ring of bulk copies, with its own reference and sums, so nothing in the
+// kernel waits for another warp; the partial results of an item that lies in
+// several ranges are merged by kv4_merge_kernel.
 //
 // Per tile: S^T = C^k q^T with 16 keys x 8 query rows to an mma (the codes are
 // the A operand), p from it in registers, transposed by movmatrix into the B
@@ -53,13 +52,13 @@ struct Kv4DecodeParams {
     const uint16_t* words[2];    // [B, Hkv, Nk]
     __nv_bfloat16* o;            // [B, Nq, H, D]
     float* lse;                  // [B, H, Nq]
-    float* o_part;               // ranges > 0: [2 ranges, ROWS, D], see kv4_range
-    float2* ml_part;             // ranges > 0: [2 ranges, ROWS] (maximum, sum), base 2
+    float* o_part;               // [2 ranges, ROWS, D] partial outputs, see kv4_span
+    float2* ml_part;             // [2 ranges, ROWS] their references and sums, base 2
     const int* seqlens_k;        // [B] or nullptr
     int B, H, Hkv, G, Nq, Nk;    // G = H / Hkv
     int causal, window;
     int row_blocks;              // blocks of ROWS query rows to a (sequence, kv head)
-    int ranges;                  // ranges the work is cut into; 0: a CTA to each item
+    int ranges;                  // ranges the work is cut into at most
     float scale_log2;
     int* error_word;
     uint64_t timeout_ns;
@@ -80,12 +79,9 @@ struct Kv4DecCfg {
     static constexpr int RING = NSTAGE * STAGE;           // a warp's
     static constexpr int SCALES = 2 * BN * 8;             // a warp's (scale, zero) of K and V
     static constexpr int OFF_SCALES = WARPS * RING;
-    static constexpr int OFF_STATS = OFF_SCALES + WARPS * SCALES;       // float4 [WARPS][ROWS]
-    static constexpr int OFF_BAR = OFF_STATS + WARPS * ROWS * 16;       // [WARPS][NSTAGE]
-    static constexpr int OFF_MISC = OFF_BAR + WARPS * NSTAGE * 8;
-    static constexpr int SMEM = OFF_MISC + 32 + WARPS * 4;
-    static constexpr int OSTRIDE = D + 4;                 // floats a row of the merge area
-    static_assert(ROWS * OSTRIDE * 4 <= RING, "a warp leaves its partial output in its ring");
+    static constexpr int OFF_BAR = OFF_SCALES + WARPS * SCALES;         // [WARPS][NSTAGE]
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * NSTAGE * 8;       // [WARPS] base, sequence, sum
+    static constexpr int SMEM = OFF_MISC + WARPS * 16 + 16;
     static_assert(STAGE % 16 == 0 && TILE % 16 == 0, "16-byte copies");
 };
 
@@ -133,7 +129,7 @@ __host__ __device__ constexpr int kv4_key(int m) { return m ^ ((m >> 1) & 1); }
 // The work is the sequence of all key tiles of all items, an item being a
 // (sequence, kv head, block of query rows) and `per` the items of a sequence.
 // Sequences differ in length, and only the device knows them, so the tiles are
-// cut into equal ranges, one a CTA; a range's ends may lie inside an item,
+// cut into equal ranges, one a warp; a range's ends may lie inside an item,
 // which then has partial results: that of the item's first tiles in slot 1 of
 // their range, all others in slot 0 of theirs (a range has at most one each).
 struct Kv4Span {
@@ -150,33 +146,16 @@ __device__ __forceinline__ Kv4Span kv4_span(const Kv4DecodeParams& p, int b) {
     return s;
 }
 
-// Ranges in use for `total` tiles: few tiles make fewer ranges than CTAs, of
-// one tile a warp at least.
-template <int WARPS>
+// Ranges in use for `total` tiles: of one tile at least.
 __device__ __forceinline__ int kv4_ranges(const Kv4DecodeParams& p, int64_t total) {
-    return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ranges), (total + WARPS - 1) / WARPS)));
+    return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ranges), total)));
 }
 
-// Index i of a lane's D / 32 values of a row as the products leave them, and
-// the channel there (channel g * D/8 + n sits at n * 8 + g).
-template <int D>
-__device__ __forceinline__ int kv4_channel(int idx) { return (idx & 7) * (D / 8) + (idx >> 3); }
-
-// A row's output from its unnormalised values (D / 32 a lane, indices lane *
-// D/32 ..), maximum and sum.
-template <int D>
-__device__ __forceinline__ void kv4_store_row(const Kv4DecodeParams& p, int b, int hk, int r,
-                                              const float (&a)[D / 32], float M, float L) {
-    const int lane = lane_id();
+// Row of [B * Nq * H] of query row r of kv head hk, and its place in lse.
+__device__ __forceinline__ size_t kv4_out_row(const Kv4DecodeParams& p, int b, int hk, int r, size_t& lse_at) {
     const int i = r / p.G, h = hk * p.G + r - i * p.G;
-    const size_t row = (static_cast<size_t>(b) * p.Nq + i) * p.H + h;
-    const bool some = !(L == 0.f);              // a NaN sum stays NaN
-    const float inv = some ? 1.f / L : 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-        p.o[row * D + kv4_channel<D>(lane * (D / 32) + e)] = __float2bfloat16(a[e] * inv);
-    if (lane == 0)
-        p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = some ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+    lse_at = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
+    return (static_cast<size_t>(b) * p.Nq + i) * p.H + h;
 }
 
 template <int D, int NT>
@@ -191,86 +170,71 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     const float kNegInf = -INFINITY;
     const int per = p.Hkv * p.row_blocks;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NSTAGE;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
-    long long* sh_base = reinterpret_cast<long long*>(smem + C::OFF_MISC + 8);
-    int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);
-    int* sh_sum = reinterpret_cast<int*>(smem + C::OFF_MISC + 32);
+    long long* sh_base = reinterpret_cast<long long*>(smem + C::OFF_MISC);
+    int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC + C::WARPS * 8);
+    int* sh_sum = sh_b + C::WARPS;
+    volatile int* abort_flag = sh_sum + C::WARPS;
     if (lane == 0) {
         for (int s = 0; s < C::NSTAGE; ++s) mbar_init(bars + s, 1);
         fence_barrier_init();
     }
     if (threadIdx.x == 0) *abort_flag = 0;
 
-    // ---------------------------------------------- this CTA's tiles --
+    // ---------------------------------------------- this warp's tiles --
     // tiles [x, x_end) of the sequence; b is the sequence of tile x and `base`
-    // its first tile
-    int64_t x = 0, x_end = 0, base = 0;
-    int b = 0;
-    if (p.ranges > 0) {
-        const int each = (p.B + C::WARPS * 32 - 1) / (C::WARPS * 32);
-        const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
-        int sum = 0;
-        for (int i = b0; i < b1; ++i) sum += kv4_span<C::BN>(p, i).n;
-        int incl = sum;
+    // its first tile.  A thread looks at B / THREADS sequences.
+    const int each = (p.B + C::WARPS * 32 - 1) / (C::WARPS * 32);
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * each), b1 = min(p.B, b0 + each);
+    int sum = 0;
+    for (int i = b0; i < b1; ++i) sum += kv4_span<C::BN>(p, i).n;
+    int incl = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sh_sum[warp] = incl;
-        __syncthreads();
-        int64_t total = 0, before = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh_sum[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, at = incl - sum;
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-            if (w == warp) before = total;
-            total += sh_sum[w];
-        }
-        total *= per;
-        const int ranges = kv4_ranges<C::WARPS>(p, total);
-        if (blockIdx.x >= ranges) return;
-        x = total * blockIdx.x / ranges;
-        x_end = total * (blockIdx.x + 1) / ranges;
-        int64_t at = (before + incl - sum) * per;
-        if (at <= x && x < at + static_cast<int64_t>(sum) * per) {
+    for (int w = 0; w < C::WARPS; ++w) {
+        if (w < warp) at += sh_sum[w];
+        total += sh_sum[w];
+    }
+    total *= per;
+    at *= per;
+    const int ranges = kv4_ranges(p, total);
+    const int range = blockIdx.x * C::WARPS + warp;
+#pragma unroll
+    for (int w = 0; w < C::WARPS; ++w) {
+        const int64_t xw = total * (blockIdx.x * C::WARPS + w) / ranges;
+        if (at <= xw && xw < at + static_cast<int64_t>(sum) * per) {
+            int64_t first = at;
             for (int i = b0; i < b1; ++i) {
-                const int64_t next = at + static_cast<int64_t>(kv4_span<C::BN>(p, i).n) * per;
-                if (x < next) {
-                    *sh_b = i;
-                    *sh_base = at;
+                const int64_t next = first + static_cast<int64_t>(kv4_span<C::BN>(p, i).n) * per;
+                if (xw < next) {
+                    sh_b[w] = i;
+                    sh_base[w] = first;
                     break;
                 }
-                at = next;
+                first = next;
             }
         }
-        __syncthreads();
-        if (x >= x_end) return;
-        b = *sh_b;
-        base = *sh_base;
-    } else {
-        // item blockIdx.x alone
-        b = blockIdx.x / per;
-        const Kv4Span s = kv4_span<C::BN>(p, b);
-        const int item = blockIdx.x - b * per;
-        if (s.n == 0) {
-            const int hk = item / p.row_blocks, r0 = (item - hk * p.row_blocks) * C::ROWS;
-            const float zero[D / 32] = {};
-            for (int r = r0 + warp; r < min(r0 + C::ROWS, p.Nq * p.G); r += C::WARPS)
-                kv4_store_row<D>(p, b, hk, r, zero, kNegInf, 0.f);
-            return;
-        }
-        x = static_cast<int64_t>(item) * s.n;
-        x_end = x + s.n;
-        __syncthreads();
     }
+    __syncthreads();
+    if (range >= ranges || total == 0) return;      // from here on each warp is on its own
+    int64_t x = total * range / ranges;
+    const int64_t x_end = total * (range + 1) / ranges;
+    int b = sh_b[warp];
+    int64_t base = sh_base[warp];
     const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
     uint8_t* ring = smem + warp * C::RING;
     float2* sck = reinterpret_cast<float2*>(smem + C::OFF_SCALES + warp * C::SCALES);
     float2* scv = sck + C::BN;
-    float4* stats = reinterpret_cast<float4*>(smem + C::OFF_STATS);     // [WARPS][ROWS] max, sum, factor
     uint32_t stage = 0, phase = 0;      // ring position over all segments
     bool ok = true;
 
-    while (x < x_end) {
+    while (x < x_end && ok) {
         // ------------------------------------------------- a segment --
         const Kv4Span sp = kv4_span<C::BN>(p, b);
         if (sp.n == 0) {
@@ -286,9 +250,8 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         const int nk = sp.nk, qpos0 = nk - p.Nq;                 // key position of query 0
 
         const int64_t head = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk;
-        const int first = sp.t0 + tile0 + warp;
-        const int ntile = ok && warp < count ? (count - warp + C::WARPS - 1) / C::WARPS : 0;
-        // what the warp's next load reads
+        const int first = sp.t0 + tile0;
+        // what the next load reads
         int64_t row_next = head + static_cast<int64_t>(first) * C::BN;
         int room_next = p.Nk - first * C::BN;
         auto load_next = [&](int slot) {
@@ -301,12 +264,12 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                 bulk_load(dst + 2 * C::TILE, p.words[0] + row_next, rows * 2, bars + slot);
                 bulk_load(dst + 2 * C::TILE + C::WORDB, p.words[1] + row_next, rows * 2, bars + slot);
             }
-            row_next += C::WARPS * C::BN;
-            room_next -= C::WARPS * C::BN;
+            row_next += C::BN;
+            room_next -= C::BN;
         };
         {
             int slot = stage;
-            for (int i = 0; i < min(C::NSTAGE, ntile); ++i) {
+            for (int i = 0; i < min(C::NSTAGE, count); ++i) {
                 load_next(slot);
                 slot = slot + 1 == C::NSTAGE ? 0 : slot + 1;
             }
@@ -383,10 +346,10 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         uint32_t ev = 6;                // biased exponent of the largest V scale so far
         float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
 
-        for (int i = 0; i < ntile; ++i) {
+        for (int i = 0; i < count; ++i) {
             if (!__all_sync(0xffffffffu, mbar_wait(bars + stage, phase, wc))) { ok = false; break; }
             const uint8_t* st = ring + stage * C::STAGE;
-            const int k0 = (first + i * C::WARPS) * C::BN;
+            const int k0 = (first + i) * C::BN;
 
             // ---- scales and zeros: a key a lane
             const bool edge = k0 + C::BN > nk;
@@ -602,12 +565,14 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                     }
             }
             __syncwarp();               // the stage may be loaded again
-            if (i + C::NSTAGE < ntile) load_next(stage);
+            if (i + C::NSTAGE < count) load_next(stage);
             stage = stage + 1 == C::NSTAGE ? 0 : stage + 1;
             phase ^= stage == 0;
         }
 
-        // ------------------------------------------- merge of the warps --
+        // ------------------------------------------------- its result --
+        // Lane (g8, t4) holds channels g8 * D/8 .. of rows nt * 8 + 2 t4 + {0, 1}.
+        const bool whole = count == sp.n;
         const float back = ldexpf(1.f, static_cast<int>(ev) - 133);       // undoes vnorm
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -618,59 +583,36 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                 za[nt].x += __shfl_xor_sync(0xffffffffu, za[nt].x, o);
                 za[nt].y += __shfl_xor_sync(0xffffffffu, za[nt].y, o);
             }
-            if (g8 == 0) {
-                float4* d = stats + warp * C::ROWS + nt * 8 + 2 * t4;
-                d[0] = make_float4(nm[nt].x == kNoRef ? kNegInf : -nm[nt].x, l[nt].x, back, 0.f);
-                d[1] = make_float4(nm[nt].y == kNoRef ? kNegInf : -nm[nt].y, l[nt].y, back, 0.f);
-            }
-        }
-        if (ntile > 0) {
-            // channel g8 * D/8 + n at n * 8 + g8: neighbouring lanes, neighbouring banks
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < 2; ++j) {
+                const int r = nt * 8 + 2 * t4 + j;
+                if (r >= nrows) continue;
+                const float L = j ? l[nt].y : l[nt].x, z = j ? za[nt].y : za[nt].x, n1 = j ? nm[nt].y : nm[nt].x;
+                const bool some = !(L == 0.f);      // a NaN sum stays NaN
+                const float f = whole ? (some ? back / L : 0.f) : back;
+                float a[D / 8];
 #pragma unroll
-                for (int m = 0; m < D / 16; ++m) {
-                    float* d0 = reinterpret_cast<float*>(ring) + (nt * 8 + 2 * t4) * C::OSTRIDE + g8 + 16 * m;
-                    float* d1 = d0 + C::OSTRIDE;
-                    d0[0] = fmaf(oacc[m][nt][0].x, 16777216.f, -za[nt].x);         // codes times 2^-24
-                    d1[0] = fmaf(oacc[m][nt][0].y, 16777216.f, -za[nt].y);
-                    d0[8] = fmaf(oacc[m][nt][1].x, 1048576.f, -za[nt].x);          // and 2^-20
-                    d1[8] = fmaf(oacc[m][nt][1].y, 1048576.f, -za[nt].y);
+                for (int m = 0; m < D / 16; ++m) {  // codes times 2^-24, and 2^-20
+                    a[2 * m] = fmaf(j ? oacc[m][nt][0].y : oacc[m][nt][0].x, 16777216.f, -z) * f;
+                    a[2 * m + 1] = fmaf(j ? oacc[m][nt][1].y : oacc[m][nt][1].x, 1048576.f, -z) * f;
                 }
-        }
-        __syncthreads();
-        const bool whole = count == sp.n;
-        for (int r = warp; r < nrows; r += C::WARPS) {
-            const float4 mine = lane < C::WARPS ? stats[lane * C::ROWS + r] : make_float4(kNegInf, 0.f, 0.f, 0.f);
-            float M = mine.x;
+                if (whole) {
+                    size_t lse_at;
+                    const size_t row = kv4_out_row(p, b, hk, r0 + r, lse_at);
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + g8 * (D / 8));
 #pragma unroll
-            for (int o = C::WARPS / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float f = mine.x == kNegInf && !isnan(mine.y) ? 0.f : ex2(mine.x - M);
-            float L = f * mine.y;
+                    for (int v = 0; v < D / 64; ++v)
+                        dst[v] = make_uint4(pack_bf16(a[8 * v], a[8 * v + 1]), pack_bf16(a[8 * v + 2], a[8 * v + 3]),
+                                            pack_bf16(a[8 * v + 4], a[8 * v + 5]), pack_bf16(a[8 * v + 6], a[8 * v + 7]));
+                    if (g8 == 0) p.lse[lse_at] = some ? (__log2f(L) - n1) * 0.6931471805599453f : -INFINITY;
+                } else {
+                    const size_t at_row = (static_cast<size_t>(range) * 2 + (tile0 == 0)) * C::ROWS + r;
+                    float4* dst = reinterpret_cast<float4*>(p.o_part + at_row * D + g8 * (D / 8));
 #pragma unroll
-            for (int o = C::WARPS / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            const float fb = f * mine.z;
-            M = __shfl_sync(0xffffffffu, M, 0);
-            L = __shfl_sync(0xffffffffu, L, 0);
-            float a[D / 32];
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) {
-                const float fw = __shfl_sync(0xffffffffu, fb, w);
-                if (fw == 0.f) continue;        // nothing there (NaN goes on)
-                const float* src = reinterpret_cast<const float*>(smem + w * C::RING) + r * C::OSTRIDE + lane * (D / 32);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) a[e] = fmaf(src[e], fw, a[e]);
-            }
-            if (whole) {
-                kv4_store_row<D>(p, b, hk, r0 + r, a, M, L);
-            } else {
-                const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (tile0 == 0)) * C::ROWS + r;
-                float* dst = p.o_part + at * D + lane * (D / 32);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) dst[e] = a[e];
-                if (lane == 0) p.ml_part[at] = make_float2(M, L);
+                    for (int v = 0; v < D / 32; ++v)
+                        dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+                    if (g8 == 0) p.ml_part[at_row] = make_float2(n1 == kNoRef ? kNegInf : -n1, L);
+                }
             }
         }
         x += count;
@@ -678,8 +620,6 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
             base = x;
             ++b;
         }
-        fence_proxy_async_smem();       // the ring's next contents come by bulk copy
-        __syncthreads();
     }
     if (!ok && lane == 0) {
         // let the copies in flight land before the CTA exits
@@ -695,15 +635,18 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
 
 // Merges the partial results of the items that lie in several ranges, and
 // writes the outputs of sequences without keys.  A CTA to a query row; its
-// warps take every fourth range.
+// warps share the ranges.
+constexpr int kKv4MergeWarps = 16;      // at most
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kKv4MergeWarps * 32)
 kv4_merge_kernel(const Kv4DecodeParams p) {
     using C = Kv4DecCfg<D, NT>;
-    constexpr int V = D / 32;
-    __shared__ float sm_a[4][D];
-    __shared__ float2 sm_ml[4];
-    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    constexpr int V = D / 32;                   // channels a lane
+    constexpr int AHEAD = 4;                    // partials read at once
+    __shared__ float sm_a[kKv4MergeWarps][D];
+    __shared__ float2 sm_ml[kKv4MergeWarps];
+    const int lane = lane_id(), warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int per = p.Hkv * p.row_blocks;
     const int rows = p.Nq * p.G;
     const int r = blockIdx.x % rows, bh = blockIdx.x / rows;
@@ -723,7 +666,7 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
     const int n = kv4_span<C::BN>(p, b).n;
     total *= per;
     at = at * per + static_cast<int64_t>(item) * n;
-    const int ranges = kv4_ranges<C::WARPS>(p, total);
+    const int ranges = kv4_ranges(p, total);
     auto range_of = [&](int64_t x) {            // the range that holds tile x
         int c = static_cast<int>(x * ranges / total);
         while (total * (c + 1) / ranges <= x) ++c;
@@ -735,15 +678,10 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
     // its results are complete.  Every thread waits, so that this grid does not
     // end before that one.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n > 0 && c0 == c1) return;              // written by the range's own warp
     float a[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) a[e] = 0.f;
-    if (n == 0) {
-        if (warp == 0) kv4_store_row<D>(p, b, hk, r, a, -INFINITY, 0.f);
-        return;
-    }
-    if (c0 == c1) return;                       // written by the range's own CTA
-    auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0)) * C::ROWS + r % C::ROWS; };
     float M = -INFINITY, L = 0.f;
     auto take = [&](float m, float sum, const float (&v)[V]) {
         if (m == -INFINITY && !isnan(sum)) return;      // no key of this row
@@ -754,32 +692,44 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
         for (int e = 0; e < V; ++e) a[e] = fmaf(v[e], w1, a[e] * w0);
         M = m_new;
     };
-    for (int c = c0 + warp; c <= c1; c += 16) {
-        float v[4][V];
-        float2 ml[4];
+    if (n > 0) {
+        auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0)) * C::ROWS + r % C::ROWS; };
+        for (int c = c0 + warp; c <= c1; c += AHEAD * warps) {
+            float v[AHEAD][V];
+            float2 ml[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t at_slot = slot(min(c + 4 * i, c1));
-            ml[i] = c + 4 * i <= c1 ? p.ml_part[at_slot] : make_float2(-INFINITY, 0.f);
+            for (int i = 0; i < AHEAD; ++i) {
+                const size_t from = slot(min(c + warps * i, c1));
+                ml[i] = c + warps * i <= c1 ? p.ml_part[from] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = p.o_part[at_slot * D + lane * V + e];
+                for (int e = 0; e < V; ++e) v[i][e] = p.o_part[from * D + lane * V + e];
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) take(ml[i].x, ml[i].y, v[i]);
         }
+        const int used = min(warps, c1 - c0 + 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) take(ml[i].x, ml[i].y, v[i]);
+        for (int e = 0; e < V; ++e) sm_a[warp][lane * V + e] = a[e];
+        if (lane == 0) sm_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < used; ++w) {
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = sm_a[w][lane * V + e];
+            take(sm_ml[w].x, sm_ml[w].y, v);
+        }
+    } else if (warp != 0) {
+        return;
     }
+    size_t lse_at;
+    const size_t row = kv4_out_row(p, b, hk, r, lse_at);
+    const bool some = !(L == 0.f);              // a NaN sum stays NaN
+    const float inv = some ? 1.f / L : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * V);
 #pragma unroll
-    for (int e = 0; e < V; ++e) sm_a[warp][lane * V + e] = a[e];
-    if (lane == 0) sm_ml[warp] = make_float2(M, L);
-    __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-        float v[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = sm_a[w][lane * V + e];
-        take(sm_ml[w].x, sm_ml[w].y, v);
-    }
-    kv4_store_row<D>(p, b, hk, r, a, M, L);
+    for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16(a[2 * e] * inv, a[2 * e + 1] * inv);
+    if (lane == 0) p.lse[lse_at] = some ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace fa

@@ -64,14 +64,13 @@ def test_attention_validation(kw, code):
 
 
 def test_sizes():
-    # one split and few rows need nothing; ranges need two partial results of
-    # 8 or 16 rows (d values, maximum, sum) each; a chunk needs its splits'
-    # partials and the bf16 rows
+    # few rows: two partial results of 8 or 16 rows (d values, reference, sum)
+    # to each range; a chunk: its splits' partials and the bf16 rows
     def up(n):
         return (n + 255) // 256 * 256
 
     size = fa.fa_fwd_kv4_workspace_size
-    assert size(2, 8, 2, 1, 512, 128, 1) == 0
+    assert size(2, 8, 2, 1, 512, 128, 1) == up(2 * (2 * 2) * 8 * 130 * 4)
     assert size(2, 8, 2, 1, 512, 128, 4) == up(2 * (4 * 2 * 2) * 8 * 130 * 4)
     assert size(2, 8, 2, 3, 512, 64, 4) == up(2 * (4 * 2 * 2) * 16 * 66 * 4)
     assert size(2, 8, 2, 7, 512, 64, 3) == up(2 * (3 * 2 * 2 * 2) * 16 * 66 * 4)
