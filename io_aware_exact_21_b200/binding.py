@@ -106,7 +106,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: torch.cuda.current_stream() makes a Stream object
+        # around it, which costs as much as the rest of a small call's checks
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -154,31 +156,29 @@ def fa_fwd_kvcache_workspace_size(B, H, Nq, d, num_splits) -> int:
 def fa_quantize_kv4(k, v, k_codes, k_words, v_codes, v_words, B, N, Hkv, Nk, d, cu_seqlens, starts,
                     lens, stream=None) -> int:
     return load_library().fa_quantize_kv4(_ptr(k), _ptr(v), _ptr(k_codes), _ptr(k_words),
-                                          _ptr(v_codes), _ptr(v_words), int(B), int(N), int(Hkv),
-                                          int(Nk), int(d), _ptr(cu_seqlens), _ptr(starts),
-                                          _ptr(lens), _stream(stream))
+                                          _ptr(v_codes), _ptr(v_words), B, N, Hkv, Nk, d,
+                                          _ptr(cu_seqlens), _ptr(starts), _ptr(lens),
+                                          _stream(stream))
 
 
 def fa_dequantize_kv4(k_codes, k_words, v_codes, v_words, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts,
                       lens, stream=None) -> int:
     return load_library().fa_dequantize_kv4(_ptr(k_codes), _ptr(k_words), _ptr(v_codes),
-                                            _ptr(v_words), _ptr(k), _ptr(v), int(B), int(N),
-                                            int(Hkv), int(Nk), int(d), _ptr(cu_seqlens),
-                                            _ptr(starts), _ptr(lens), _stream(stream))
+                                            _ptr(v_words), _ptr(k), _ptr(v), B, N, Hkv, Nk, d,
+                                            _ptr(cu_seqlens), _ptr(starts), _ptr(lens),
+                                            _stream(stream))
 
 
 def fa_fwd_kv4(q, k_codes, k_words, v_codes, v_words, o, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
                window, seqlens_k, num_splits, workspace, workspace_bytes, stream=None) -> int:
     return load_library().fa_fwd_kv4(_ptr(q), _ptr(k_codes), _ptr(k_words), _ptr(v_codes),
-                                     _ptr(v_words), _ptr(o), _ptr(lse), int(B), int(H), int(Hkv),
-                                     int(Nq), int(Nk), int(d), float(scale), int(causal),
-                                     int(window), _ptr(seqlens_k), int(num_splits),
-                                     _ptr(workspace), int(workspace_bytes), _stream(stream))
+                                     _ptr(v_words), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d, scale,
+                                     causal, window, _ptr(seqlens_k), num_splits, _ptr(workspace),
+                                     workspace_bytes, _stream(stream))
 
 
 def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits) -> int:
-    return int(load_library().fa_fwd_kv4_workspace_size(int(B), int(H), int(Hkv), int(Nq), int(Nk),
-                                                        int(d), int(num_splits)))
+    return load_library().fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
 
 
 def fa_fp8_vt_bytes(B, H, N, d) -> int:
@@ -297,6 +297,15 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+def _fits(t, name, shape, dtype, device, index):
+    """_expect for the calls of a decode step, where the checks are a good part
+    of the time: one look when the tensor is right (index: the CUDA device's),
+    and _expect's message when it is not."""
+    if not (index >= 0 and t is not None and t.shape == shape and t.dtype is dtype
+            and t.get_device() == index and t.is_contiguous()):
+        _expect(t, name, shape, dtype, device)
 
 
 def _expect_bytes(t, name, nbytes, device):
@@ -446,26 +455,27 @@ def kv4_cache(B, rows, Hkv, d, device="cuda"):
             torch.zeros((B, Hkv, Nk), dtype=torch.int16, device=device) for n in KV4_NAMES}
 
 
-def _kv4_shape(cache, device):
-    """(B, Hkv, Nk, d) of a 4-bit cache, its tensors checked against each other."""
+def _kv4_shape(cache, device, index):
+    """A 4-bit cache's arrays, checked against each other, and (B, Hkv, Nk, d)."""
     import torch
-    for n in KV4_NAMES:
-        if cache.get(n) is None:
-            raise ValueError("cache[%r] is required" % n)
-    _rank(cache["k_codes"], "k_codes", (4,))
-    B, Hkv, Nk, half = cache["k_codes"].shape
-    for n in KV4_NAMES:
-        if n.endswith("codes"):
-            _expect(cache[n], n, (B, Hkv, Nk, half), torch.uint8, device)
-        else:
-            _expect(cache[n], n, (B, Hkv, Nk), torch.int16, device)
-    return B, Hkv, Nk, 2 * half
+    kc, kw, vc, vw = cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"), cache.get("v_words")
+    _rank(kc, "k_codes", (4,))
+    codes = kc.shape
+    words = codes[:3]
+    _fits(kc, "k_codes", codes, torch.uint8, device, index)
+    _fits(kw, "k_words", words, torch.int16, device, index)
+    _fits(vc, "v_codes", codes, torch.uint8, device, index)
+    _fits(vw, "v_words", words, torch.int16, device, index)
+    # the library launches on the current device and its stream
+    if index >= 0 and index != torch.cuda.current_device():
+        raise ValueError("the tensors are on %s, the current device is cuda:%d"
+                         % (device, torch.cuda.current_device()))
+    return (kc, kw, vc, vw), codes[0], codes[1], codes[2], 2 * codes[3]
 
 
-def _kv4_rows(t, B, Hkv, d, cu_seqlens, starts, lens):
+def _kv4_rows(t, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index):
     """Checks the rows' side of a write or read; returns its N argument."""
     import torch
-    dev = t.device
     if cu_seqlens is None:
         _rank(t, "k", (4,))
         N = t.shape[1]
@@ -476,11 +486,14 @@ def _kv4_rows(t, B, Hkv, d, cu_seqlens, starts, lens):
         _rank(t, "k (packed)", (3,))
         N = t.shape[0]
         shape = (N, Hkv, d)
-        _expect(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
-    for x, name in ((starts, "starts"), (lens, "lens")):
-        if x is not None:
-            _expect(x, name, (B,), torch.int32, dev)
-    return N, shape
+        _fits(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev, index)
+    if starts is not None:
+        _fits(starts, "starts", (B,), torch.int32, dev, index)
+    if lens is not None:
+        _fits(lens, "lens", (B,), torch.int32, dev, index)
+    _fits(t, "k", shape, torch.bfloat16, dev, index)
+    _fits(v, "v", shape, torch.bfloat16, dev, index)
+    return N
 
 
 def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=None):
@@ -489,14 +502,12 @@ def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=No
     CUDA tensor, None for 0), the first ``lens[b]`` rows of each (None for
     all); or packed [T, Hkv, d] with int32 ``cu_seqlens``.  Rows that fall
     outside the cache are left out.  Returns the cache."""
-    import torch
     _rank(k, "k", (3, 4))
-    B, Hkv, Nk, d = _kv4_shape(cache, k.device)
-    N, shape = _kv4_rows(k, B, Hkv, d, cu_seqlens, starts, lens)
-    for t, name in ((k, "k"), (v, "v")):
-        _expect(t, name, shape, torch.bfloat16, k.device)
-    _check(fa_quantize_kv4(k, v, *(cache[n] for n in KV4_NAMES), B, N, Hkv, Nk, d, cu_seqlens, starts,
-                           lens, stream), "fa_quantize_kv4")
+    dev, index = k.device, k.get_device()
+    arrays, B, Hkv, Nk, d = _kv4_shape(cache, dev, index)
+    N = _kv4_rows(k, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index)
+    _check(fa_quantize_kv4(k, v, *arrays, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
+           "fa_quantize_kv4")
     return cache
 
 
@@ -506,23 +517,22 @@ def dequantize_kv4(cache, rows=None, starts=None, lens=None, cu_seqlens=None, ou
     ``cu_seqlens``; starts and lens as quantize_kv4.  Rows that belong to no
     sequence or fall outside the cache keep what ``out`` holds (zeros when it
     is not given)."""
-    import torch
-    dev = cache["k_codes"].device
-    B, Hkv, Nk, d = _kv4_shape(cache, dev)
+    _rank(cache.get("k_codes"), "k_codes", (4,))
+    dev, index = cache["k_codes"].device, cache["k_codes"].get_device()
+    arrays, B, Hkv, Nk, d = _kv4_shape(cache, dev, index)
     if out is None:
+        import torch
         if rows is None and cu_seqlens is not None:
             raise ValueError("a packed read needs rows or out")
         n = Nk if rows is None else rows
         shape = (B, n, Hkv, d) if cu_seqlens is None else (n, Hkv, d)
         out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
     k, v = out
-    N, shape = _kv4_rows(k, B, Hkv, d, cu_seqlens, starts, lens)
+    N = _kv4_rows(k, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index)
     if rows is not None and rows != N:
         raise ValueError("out holds %d rows, rows is %d" % (N, rows))
-    for t, name in ((k, "k"), (v, "v")):
-        _expect(t, name, shape, torch.bfloat16, dev)
-    _check(fa_dequantize_kv4(*(cache[n] for n in KV4_NAMES), k, v, B, N, Hkv, Nk, d, cu_seqlens,
-                             starts, lens, stream), "fa_dequantize_kv4")
+    _check(fa_dequantize_kv4(*arrays, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
+           "fa_dequantize_kv4")
     return k, v
 
 
@@ -534,32 +544,34 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
     are the last Nq of those positions.  Returns (O, LSE)."""
     import torch
     _rank(q, "q", (4,))
-    B, Nq, H, d = q.shape
-    dev = q.device
-    _expect(q, "q", q.shape, torch.bfloat16, dev)
-    cB, Hkv, Nk, cd = _kv4_shape(cache, dev)
-    if (cB, cd) != (B, d):
+    B, Nq, H, d = shape = q.shape
+    dev, index = q.device, q.get_device()
+    _fits(q, "q", shape, torch.bfloat16, dev, index)
+    arrays, cB, Hkv, Nk, cd = _kv4_shape(cache, dev, index)
+    if cB != B or cd != d:
         raise ValueError("the cache holds %d sequences of d = %d, q has %d of %d" % (cB, cd, B, d))
     if Hkv == 0 or H % Hkv:
         raise ValueError("q has %d heads, not a multiple of the cache's %d" % (H, Hkv))
     if seqlens_k is not None:
-        _expect(seqlens_k, "seqlens_k", (B,), torch.int32, dev)
+        _fits(seqlens_k, "seqlens_k", (B,), torch.int32, dev, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _fits(out, "out", shape, torch.bfloat16, dev, index)
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
-    _expect(out, "out", q.shape, torch.bfloat16, dev)
-    _expect(lse, "lse", (B, H, Nq), torch.float32, dev)
+    else:
+        _fits(lse, "lse", (B, H, Nq), torch.float32, dev, index)
     need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, dev)
-    _check(fa_fwd_kv4(q, *(cache[n] for n in KV4_NAMES), out, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
-                      window, seqlens_k, num_splits, workspace, 0 if workspace is None else workspace.numel(),
-                      stream), "fa_fwd_kv4")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(fa_fwd_kv4(q, *arrays, out, lse, B, H, Hkv, Nq, Nk, d, scale, causal, window, seqlens_k,
+                      num_splits, workspace, 0 if workspace is None else workspace.numel(), stream),
+           "fa_fwd_kv4")
     return out, lse
 
 

@@ -459,11 +459,14 @@ int64_t kv4_row_blocks(int64_t rows) {
 }
 
 // Ranges that kv4_decode_kernel cuts its work into: the warps that run at once
-// on all SMs (12 an SM), or num_splits to an item.
+// on all SMs, or num_splits to an item.
 int kv4_range_count(int B, int Hkv, int Nq, int group, int num_splits, int num_sms) {
-    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(static_cast<int64_t>(Nq) * group);
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
     if (num_splits > 0) return static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20));
-    return 12 * num_sms;
+    using C1 = fa::Kv4DecCfg<128, 1>;
+    using C2 = fa::Kv4DecCfg<128, 2>;
+    return num_sms * (kv4_block_rows(rows) == 8 ? C1::WARPS * C1::MIN_CTAS : C2::WARPS * C2::MIN_CTAS);
 }
 
 int current_sms() {
@@ -848,8 +851,8 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     const int group = H / Hkv;
     if (rows_q > (int64_t{1} << 31) - 1 || rows_q * H * d > (int64_t{1} << 40) ||
         (kv4_direct(Nq, group, Nk) && rows_q * H > (int64_t{1} << 31) - 1) ||
-        static_cast<int64_t>(B) * Hkv * fa::kDecMaxSplits * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
-            (int64_t{1} << 31) - 1)
+        (kv4_direct(Nq, group, Nk) && static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
+                                          (int64_t{1} << 31) - 1))      // its key tiles are counted in 32 bits
         return FA_ERR_BAD_SHAPE;
     if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
     if (misaligned(q) || misaligned(k_codes) || misaligned(k_words) || misaligned(v_codes) ||

@@ -67,22 +67,23 @@ struct Kv4DecodeParams {
 template <int D, int NT>
 struct Kv4DecCfg {
     static constexpr int BN = NT == 1 ? 64 : 32;          // keys a tile
-    static constexpr int ROWS = 8 * NT;                   // query rows a CTA
-    static constexpr int WARPS = 4;
-    static constexpr int MIN_CTAS = 3;
-    static constexpr int NSTAGE = NT == 1 ? 2 : 4;
+    static constexpr int ROWS = 8 * NT;                   // query rows a warp
+    static constexpr int WARPS = 4;                       // a CTA
+    static constexpr int MIN_CTAS = 3;                    // an SM
+    static constexpr int NK = NT == 1 ? 1 : 2;            // K stages of a warp's ring
+    static constexpr int NV = NT == 1 ? 1 : 2;            // V stages
     static constexpr int MT = BN / 16;                    // mma key tiles
     static constexpr int ROWB = D / 2;                    // bytes of a row's codes
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
-    static constexpr int STAGE = 2 * TILE + 2 * WORDB;
-    static constexpr int RING = NSTAGE * STAGE;           // a warp's
-    static constexpr int SCALES = 2 * BN * 8;             // a warp's (scale, zero) of K and V
-    static constexpr int OFF_SCALES = WARPS * RING;
-    static constexpr int OFF_BAR = OFF_SCALES + WARPS * SCALES;         // [WARPS][NSTAGE]
-    static constexpr int OFF_MISC = OFF_BAR + WARPS * NSTAGE * 8;       // [WARPS] base, sequence, sum
-    static constexpr int SMEM = OFF_MISC + WARPS * 16 + 16;
-    static_assert(STAGE % 16 == 0 && TILE % 16 == 0, "16-byte copies");
+    static constexpr int KSTAGE = TILE + 2 * WORDB;       // K codes, K words, V words
+    static constexpr int OFF_V = NK * KSTAGE;
+    static constexpr int OFF_SCALES = OFF_V + NV * TILE;
+    static constexpr int WARP_BYTES = OFF_SCALES + 2 * BN * 8;          // (scale, zero) of K and V last
+    static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][NK + NV]
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * (NK + NV) * 8;
+    static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16;
+    static_assert(KSTAGE % 16 == 0 && TILE % 16 == 0 && WARP_BYTES % 16 == 0, "16-byte copies");
 };
 
 __device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -146,10 +147,21 @@ __device__ __forceinline__ Kv4Span kv4_span(const Kv4DecodeParams& p, int b) {
     return s;
 }
 
-// Ranges in use for `total` tiles: of one tile at least.
-__device__ __forceinline__ int kv4_ranges(const Kv4DecodeParams& p, int64_t total) {
-    return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ranges), total)));
-}
+// The cut of `total` tiles (below 2^31) into ranges of q or, the first rem,
+// q + 1 tiles; fewer ranges than p.ranges when there are fewer tiles.
+struct Kv4Cut {
+    int ranges, q, rem;
+    __device__ __forceinline__ Kv4Cut(const Kv4DecodeParams& p, int total) {
+        ranges = max(1, min(p.ranges, total));
+        q = total / ranges;
+        rem = total - q * ranges;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int range_of(int x) const {
+        const int cut = rem * (q + 1);
+        return x < cut ? x / (q + 1) : rem + (x - cut) / q;
+    }
+};
 
 // Row of [B * Nq * H] of query row r of kv head hk, and its place in lse.
 __device__ __forceinline__ size_t kv4_out_row(const Kv4DecodeParams& p, int b, int hk, int r, size_t& lse_at) {
@@ -169,13 +181,14 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     const int g8 = lane >> 2, t4 = lane & 3;
     const float kNegInf = -INFINITY;
     const int per = p.Hkv * p.row_blocks;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NSTAGE;
-    long long* sh_base = reinterpret_cast<long long*>(smem + C::OFF_MISC);
-    int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC + C::WARPS * 8);
-    int* sh_sum = sh_b + C::WARPS;
+    uint64_t* kbar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * (C::NK + C::NV);
+    uint64_t* vbar = kbar + C::NK;
+    int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC);
+    int* sh_base = sh_b + C::WARPS;
+    int* sh_sum = sh_base + C::WARPS;
     volatile int* abort_flag = sh_sum + C::WARPS;
     if (lane == 0) {
-        for (int s = 0; s < C::NSTAGE; ++s) mbar_init(bars + s, 1);
+        for (int s = 0; s < C::NK + C::NV; ++s) mbar_init(kbar + s, 1);
         fence_barrier_init();
     }
     if (threadIdx.x == 0) *abort_flag = 0;
@@ -195,7 +208,7 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     }
     if (lane == 31) sh_sum[warp] = incl;
     __syncthreads();
-    int64_t total = 0, at = incl - sum;
+    int total = 0, at = incl - sum;
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
         if (w < warp) at += sh_sum[w];
@@ -203,15 +216,15 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     }
     total *= per;
     at *= per;
-    const int ranges = kv4_ranges(p, total);
+    const Kv4Cut cut(p, total);
     const int range = blockIdx.x * C::WARPS + warp;
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-        const int64_t xw = total * (blockIdx.x * C::WARPS + w) / ranges;
-        if (at <= xw && xw < at + static_cast<int64_t>(sum) * per) {
-            int64_t first = at;
+        const int xw = cut.start(blockIdx.x * C::WARPS + w);
+        if (at <= xw && xw < at + sum * per) {
+            int first = at;
             for (int i = b0; i < b1; ++i) {
-                const int64_t next = first + static_cast<int64_t>(kv4_span<C::BN>(p, i).n) * per;
+                const int next = first + kv4_span<C::BN>(p, i).n * per;
                 if (xw < next) {
                     sh_b[w] = i;
                     sh_base[w] = first;
@@ -222,16 +235,16 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         }
     }
     __syncthreads();
-    if (range >= ranges || total == 0) return;      // from here on each warp is on its own
-    int64_t x = total * range / ranges;
-    const int64_t x_end = total * (range + 1) / ranges;
+    if (range >= cut.ranges || total == 0) return;      // from here on each warp is on its own
+    int x = cut.start(range);
+    const int x_end = cut.start(range + 1);
     int b = sh_b[warp];
-    int64_t base = sh_base[warp];
+    int base = sh_base[warp];
     const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
-    uint8_t* ring = smem + warp * C::RING;
-    float2* sck = reinterpret_cast<float2*>(smem + C::OFF_SCALES + warp * C::SCALES);
+    uint8_t* ring = smem + warp * C::WARP_BYTES;
+    float2* sck = reinterpret_cast<float2*>(ring + C::OFF_SCALES);
     float2* scv = sck + C::BN;
-    uint32_t stage = 0, phase = 0;      // ring position over all segments
+    uint32_t ks = 0, kp = 0, vs = 0, vp = 0;        // ring stage and phase of K and V, over all segments
     bool ok = true;
 
     while (x < x_end && ok) {
@@ -241,39 +254,44 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
             ++b;
             continue;
         }
-        const int item = static_cast<int>((x - base) / sp.n);
-        const int tile0 = static_cast<int>((x - base) - static_cast<int64_t>(item) * sp.n);
-        const int count = static_cast<int>(min(static_cast<int64_t>(sp.n - tile0), x_end - x));
+        const int item = (x - base) / sp.n;
+        const int tile0 = x - base - item * sp.n;
+        const int count = min(sp.n - tile0, x_end - x);
         const int hk = item / p.row_blocks;
         const int r0 = (item - hk * p.row_blocks) * C::ROWS;     // first of the query rows
         const int nrows = min(C::ROWS, p.Nq * p.G - r0);
         const int nk = sp.nk, qpos0 = nk - p.Nq;                 // key position of query 0
 
-        const int64_t head = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk;
         const int first = sp.t0 + tile0;
-        // what the next load reads
-        int64_t row_next = head + static_cast<int64_t>(first) * C::BN;
-        int room_next = p.Nk - first * C::BN;
-        auto load_next = [&](int slot) {
+        const int64_t row0 = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk + static_cast<int64_t>(first) * C::BN;
+        const int room = p.Nk - first * C::BN;
+        // loads of the segment's tile i: K with both words, and V (rows to be
+        // read are a multiple of 8)
+        auto load_k = [&](int i, uint32_t stage) {
             if (lane == 0) {
-                const uint32_t rows = min(C::BN, room_next);     // a multiple of 8
-                uint8_t* dst = ring + slot * C::STAGE;
-                mbar_arrive_expect_tx(bars + slot, rows * (2 * C::ROWB + 4));
-                bulk_load(dst, p.codes[0] + row_next * C::ROWB, rows * C::ROWB, bars + slot);
-                bulk_load(dst + C::TILE, p.codes[1] + row_next * C::ROWB, rows * C::ROWB, bars + slot);
-                bulk_load(dst + 2 * C::TILE, p.words[0] + row_next, rows * 2, bars + slot);
-                bulk_load(dst + 2 * C::TILE + C::WORDB, p.words[1] + row_next, rows * 2, bars + slot);
+                const uint32_t rows = min(C::BN, room - i * C::BN);
+                const int64_t row = row0 + i * C::BN;
+                uint8_t* dst = ring + stage * C::KSTAGE;
+                mbar_arrive_expect_tx(kbar + stage, rows * (C::ROWB + 4));
+                bulk_load(dst, p.codes[0] + row * C::ROWB, rows * C::ROWB, kbar + stage);
+                bulk_load(dst + C::TILE, p.words[0] + row, rows * 2, kbar + stage);
+                bulk_load(dst + C::TILE + C::WORDB, p.words[1] + row, rows * 2, kbar + stage);
             }
-            row_next += C::BN;
-            room_next -= C::BN;
         };
-        {
-            int slot = stage;
-            for (int i = 0; i < min(C::NSTAGE, count); ++i) {
-                load_next(slot);
-                slot = slot + 1 == C::NSTAGE ? 0 : slot + 1;
+        auto load_v = [&](int i, uint32_t stage) {
+            if (lane == 0) {
+                const uint32_t rows = min(C::BN, room - i * C::BN);
+                mbar_arrive_expect_tx(vbar + stage, rows * C::ROWB);
+                bulk_load(ring + C::OFF_V + stage * C::TILE, p.codes[1] + (row0 + i * C::BN) * C::ROWB, rows * C::ROWB,
+                          vbar + stage);
             }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < C::NK; ++i)
+            if (i < count) load_k(i, ks + i < C::NK ? ks + i : ks + i - C::NK);
+#pragma unroll
+        for (int i = 0; i < C::NV; ++i)
+            if (i < count) load_v(i, vs + i < C::NV ? vs + i : vs + i - C::NV);
 
         // ------------------------------------- queries as B fragments --
         // Row nt * 8 + g8, channels t4 * D/4 ..: of word w (8 codes), pair u of
@@ -347,14 +365,14 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
 
         for (int i = 0; i < count; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(bars + stage, phase, wc))) { ok = false; break; }
-            const uint8_t* st = ring + stage * C::STAGE;
+            if (!__all_sync(0xffffffffu, mbar_wait(kbar + ks, kp, wc))) { ok = false; break; }
+            const uint8_t* st = ring + ks * C::KSTAGE;
             const int k0 = (first + i) * C::BN;
 
             // ---- scales and zeros: a key a lane
             const bool edge = k0 + C::BN > nk;
             {
-                const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + 2 * C::TILE);
+                const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + C::TILE);
                 uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
 #pragma unroll
                 for (int kk = 0; kk < C::BN / 32; ++kk) {
@@ -402,8 +420,14 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
             }
             __syncwarp();
 
+            // ---- scores, and p = 2^(x - reference).  A lane's sum over the tile tells
+            // when a score has passed the reference by so much that p s^v could
+            // leave fp16: then the scores are formed again (they are not kept), the
+            // reference moves to their maximum, and p is taken anew.
+            float2 e[C::MT][NT][2], ts[NT];
+            for (bool move = false;; move = true) {
+            float2 (&s)[C::MT][NT][2] = e;
             // ---- S^T = C^k q^T: keys x 8 NT rows
-            float2 s[C::MT][NT][2];
 #pragma unroll
             for (int m = 0; m < C::MT; ++m) {
                 uint32_t ka[W], kb[W];
@@ -457,25 +481,8 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                         }
                     }
             }
-            // ---- p = 2^(x - reference).  A lane's sum over the tile tells when a
-            // score has passed the reference by so much that p s^v could leave
-            // fp16: then the reference moves to the maximum and p is taken anew.
-            float2 e[C::MT][NT][2], ts[NT];
-            bool over = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                ts[nt] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
-                        e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
-                        ts[nt] = fadd2(ts[nt], e[m][nt][half]);
-                    }
-                over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
-            }
-            if (__any_sync(0xffffffffu, over)) {
+
+            if (move) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float2 mx = s[0][nt][0];
@@ -504,17 +511,28 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                         oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
                         oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
                     }
-                    ts[nt] = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
-                            e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
-                            ts[nt] = fadd2(ts[nt], e[m][nt][half]);
-                        }
                 }
             }
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                ts[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
+                        e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
+                        ts[nt] = fadd2(ts[nt], e[m][nt][half]);
+                    }
+                over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
+            }
+            if (move || !__any_sync(0xffffffffu, over)) break;
+            }
+            __syncwarp();               // this K stage may be loaded again
+            if (i + C::NK < count) load_k(i + C::NK, ks);
+            ks = ks + 1 == C::NK ? 0 : ks + 1;
+            kp ^= ks == 0;
             // ---- p s^v as the B fragments of the second product
             uint32_t pf[C::MT][NT][2];
 #pragma unroll
@@ -532,6 +550,8 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                     }
                 }
             // ---- O^T += C^v (p s^v)^T
+            if (!__all_sync(0xffffffffu, mbar_wait(vbar + vs, vp, wc))) { ok = false; break; }
+            const uint8_t* sv = ring + C::OFF_V + vs * C::TILE;
 #pragma unroll
             for (int m = 0; m < C::MT; ++m) {
                 constexpr int VW = D / 64;                 // words of codes a lane and key
@@ -539,7 +559,7 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const int row = m * 16 + (kk >> 1) * 8 + kv4_key(2 * t4 + (kk & 1));
-                    const uint8_t* src = st + C::TILE + row * C::ROWB + g8 * (VW * 4);
+                    const uint8_t* src = sv + row * C::ROWB + g8 * (VW * 4);
                     if constexpr (D == 128) {
                         const uint2 u = *reinterpret_cast<const uint2*>(src);
                         v[kk][0] = u.x;
@@ -564,10 +584,10 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
                         }
                     }
             }
-            __syncwarp();               // the stage may be loaded again
-            if (i + C::NSTAGE < count) load_next(stage);
-            stage = stage + 1 == C::NSTAGE ? 0 : stage + 1;
-            phase ^= stage == 0;
+            __syncwarp();               // this V stage may be loaded again
+            if (i + C::NV < count) load_v(i + C::NV, vs);
+            vs = vs + 1 == C::NV ? 0 : vs + 1;
+            vp ^= vs == 0;
         }
 
         // ------------------------------------------------- its result --
@@ -616,7 +636,7 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
             }
         }
         x += count;
-        if (x - base == static_cast<int64_t>(sp.n) * per) {
+        if (x - base == sp.n * per) {
             base = x;
             ++b;
         }
@@ -625,10 +645,15 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         // let the copies in flight land before the CTA exits
         volatile int no_abort = 0;
         const WaitCtl dw{&no_abort, p.error_word, 200000000ull};
-        for (int s = 0; s < C::NSTAGE; ++s) {
-            mbar_wait(bars + stage, phase, dw);
-            stage = stage + 1 == C::NSTAGE ? 0 : stage + 1;
-            phase ^= stage == 0;
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_wait(kbar + ks, kp, dw);
+            ks = ks + 1 == C::NK ? 0 : ks + 1;
+            kp ^= ks == 0;
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_wait(vbar + vs, vp, dw);
+            vs = vs + 1 == C::NV ? 0 : vs + 1;
+            vp ^= vs == 0;
         }
     }
 }
@@ -652,28 +677,18 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
     const int r = blockIdx.x % rows, bh = blockIdx.x / rows;
     const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
     const int item = hk * p.row_blocks + r / C::ROWS;
-    int64_t total = 0, at = 0;
+    int total = 0, at = 0;
     for (int i = lane; i < p.B; i += 32) {
         const int n = kv4_span<C::BN>(p, i).n;
         total += n;
         if (i < b) at += n;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        at += __shfl_xor_sync(0xffffffffu, at, o);
-    }
+    total = __reduce_add_sync(0xffffffffu, total) * per;
+    at = __reduce_add_sync(0xffffffffu, at) * per;
     const int n = kv4_span<C::BN>(p, b).n;
-    total *= per;
-    at = at * per + static_cast<int64_t>(item) * n;
-    const int ranges = kv4_ranges(p, total);
-    auto range_of = [&](int64_t x) {            // the range that holds tile x
-        int c = static_cast<int>(x * ranges / total);
-        while (total * (c + 1) / ranges <= x) ++c;
-        while (total * c / ranges > x) --c;
-        return c;
-    };
-    const int c0 = n > 0 ? range_of(at) : 0, c1 = n > 0 ? range_of(at + n - 1) : 0;
+    at += item * n;
+    const Kv4Cut cut(p, total);
+    const int c0 = n > 0 ? cut.range_of(at) : 0, c1 = n > 0 ? cut.range_of(at + n - 1) : 0;
     // launched as a programmatic dependent of the kernel above: from here on
     // its results are complete.  Every thread waits, so that this grid does not
     // end before that one.
