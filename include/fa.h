@@ -233,9 +233,9 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  *   num_splits : few rows: the keys of all sequences and heads together are
  * cut into equal ranges, num_splits to each (sequence, key/value head) on
  * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.
- *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
- * bytes (for num_splits = 0 they are those of the current device), 16-byte
- * aligned; contents on entry do not matter.  Calls that may overlap on the GPU
+ *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window,
+ * num_splits) bytes (for num_splits = 0 they are those of the current device;
+ * where they are 0 it may be NULL), 16-byte aligned; contents on entry do not matter.  Calls that may overlap on the GPU
  * need one each.
  * Errors as fa_fwd_kvcache; H not a multiple of Hkv is FA_ERR_BAD_SHAPE.
  */
@@ -246,7 +246,8 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
                       const void* v_words, void* k, void* v, int B, int N, int Hkv, int Nk, int d,
                       const int* cu_seqlens, const int* starts, const int* lens,
                       cudaStream_t stream);
-size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits);
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window,
+                                 int num_splits);
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
                const void* v_words, void* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
                float scale, int causal, int window, const int* seqlens_k, int num_splits,

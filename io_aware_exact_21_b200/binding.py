@@ -39,7 +39,7 @@ SIGNATURES = {
                                _VP]),
     "fa_fwd_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP,
                         _I, _VP, _SZ, _VP]),
-    "fa_fwd_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "fa_fwd_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "fa_bwd_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_bwd": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _I,
                     _VP, _VP, _SZ, _VP]),
@@ -177,8 +177,8 @@ def fa_fwd_kv4(q, k_codes, k_words, v_codes, v_words, o, lse, B, H, Hkv, Nq, Nk,
                                      workspace_bytes, _stream(stream))
 
 
-def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits) -> int:
-    return load_library().fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
+def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits) -> int:
+    return load_library().fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
 
 
 def fa_fp8_vt_bytes(B, H, N, d) -> int:
@@ -564,7 +564,7 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
     else:
         _fits(lse, "lse", (B, H, Nq), torch.float32, dev, index)
-    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits)
+    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, dev)
     elif need:

@@ -105,7 +105,8 @@ cudaError_t decode_set_smem_limits() {
 
 template <int D, int NT>
 cudaError_t kv4_set_smem_limit() {
-    return allow_smem(fa::kv4_decode_kernel<D, NT>, fa::Kv4DecCfg<D, NT>::SMEM);
+    const cudaError_t e = allow_smem(fa::kv4_decode_kernel<D, NT>, fa::Kv4DecCfg<D, NT>::SMEM);
+    return e == cudaSuccess ? allow_smem(fa::kv4_cluster_kernel<D, NT>, fa::Kv4DecCfg<D, NT>::SMEM) : e;
 }
 
 cudaError_t kv4_set_smem_limits() {
@@ -442,6 +443,9 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
 }
 
 // ------------------------------------------------------ 4-bit K/V cache --
+#ifndef KV4_CLUSTER_TILES
+#define KV4_CLUSTER_TILES 4
+#endif
 constexpr int kKv4DirectRows = 32;
 
 // Whether attention over the 4-bit cache runs on kv4_decode_kernel (query rows
@@ -458,15 +462,25 @@ int64_t kv4_row_blocks(int64_t rows) {
     return (rows + per - 1) / per;
 }
 
-// Ranges that kv4_decode_kernel cuts its work into: the warps that run at once
-// on all SMs, or num_splits to an item.
-int kv4_range_count(int B, int Hkv, int Nq, int group, int num_splits, int num_sms) {
-    const int64_t rows = static_cast<int64_t>(Nq) * group;
-    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
-    if (num_splits > 0) return static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20));
+// How the key tiles are dealt out: to a cluster of `cluster` CTAs each item, or
+// (cluster 0) in `ranges` equal ranges, with a merge after it.
+struct Kv4Plan {
+    int cluster, ranges;
+};
+
+Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_splits, int num_sms) {
     using C1 = fa::Kv4DecCfg<128, 1>;
     using C2 = fa::Kv4DecCfg<128, 2>;
-    return num_sms * (kv4_block_rows(rows) == 8 ? C1::WARPS * C1::MIN_CTAS : C2::WARPS * C2::MIN_CTAS);
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
+    if (num_splits > 0) return {0, static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20))};
+    const int ctas = num_sms * (kv4_block_rows(rows) == 8 ? C1::MIN_CTAS : C2::MIN_CTAS);
+    const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq + C1::BN) : Nk;
+    const int64_t tiles = (keys + C1::BN - 1) / C1::BN;
+    int cluster = 8;
+    while (cluster > 1 && (items * cluster > ctas || tiles <= C1::WARPS * cluster / 2)) cluster /= 2;
+    if (items * cluster <= ctas && tiles <= KV4_CLUSTER_TILES * C1::WARPS * cluster) return {cluster, 0};
+    return {0, ctas * C1::WARPS};
 }
 
 int current_sms() {
@@ -484,17 +498,17 @@ size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
 
 // Bytes of the partial results: of the ranges (two of ROWS rows, each with its
 // maximum and sum), or of a chunk's splits.
-size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits, int num_sms) {
+size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const int group = H / Hkv;
     if (!kv4_direct(Nq, group, Nk))
         return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
-    const size_t rows = 2 * static_cast<size_t>(kv4_range_count(B, Hkv, Nq, group, num_splits, num_sms)) *
+    const size_t rows = 2 * static_cast<size_t>(kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms).ranges) *
                         kv4_block_rows(static_cast<int64_t>(Nq) * group);
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
 
-size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits, int num_sms) {
-    const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, num_splits, num_sms);
+size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
+    const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
     return kv4_direct(Nq, H / Hkv, Nk) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
 }
 
@@ -570,8 +584,27 @@ int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_wo
 }
 
 template <int D, int NT>
-int launch_kv4_decode(const fa::Kv4DecodeParams& p, cudaStream_t stream) {
+int launch_kv4_decode(const fa::Kv4DecodeParams& p, const Kv4Plan& plan, cudaStream_t stream) {
     using C = fa::Kv4DecCfg<D, NT>;
+    const int items = p.B * p.Hkv * p.row_blocks;
+    if (plan.cluster > 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(items * plan.cluster));
+        cfg.blockDim = dim3(C::WARPS * 32);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(plan.cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const int slot = prof_start(4, stream);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::kv4_cluster_kernel<D, NT>, p);
+        prof_stop(4, slot, stream);
+        return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    }
     const int grid = (p.ranges + C::WARPS - 1) / C::WARPS;
     const int slot = prof_start(4, stream);
     fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(p);
@@ -582,7 +615,6 @@ int launch_kv4_decode(const fa::Kv4DecodeParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Nq * p.H));
     // as many warps as bring an item's partials in with one or two waits
-    const int items = p.B * p.Hkv * p.row_blocks;
     cfg.blockDim = dim3(p.ranges / items >= 32 ? 32 * fa::kKv4MergeWarps : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -831,9 +863,9 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
                            lens, stream);
 }
 
-size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int num_splits) {
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits) {
     if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0 || num_splits < 0) return 0;
-    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, num_splits, current_sms());
+    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, current_sms());
 }
 
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
@@ -860,7 +892,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
         return FA_ERR_MISALIGNED;
     if (rows_q == 0) return FA_OK;
-    const size_t need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, num_splits);
+    const size_t need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
     if (need > 0 && misaligned(workspace)) return FA_ERR_MISALIGNED;
     DeviceState* st = nullptr;
@@ -917,15 +949,16 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.window = window > 0 ? window : 0;
     const int64_t rows = static_cast<int64_t>(Nq) * group;
     p.row_blocks = static_cast<int>(kv4_row_blocks(rows));
-    p.ranges = kv4_range_count(B, Hkv, Nq, group, num_splits, st->num_sms);
+    const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, st->num_sms);
+    p.ranges = plan.ranges;
     p.o_part = part;
     p.ml_part = reinterpret_cast<float2*>(part + 2 * static_cast<size_t>(p.ranges) * kv4_block_rows(rows) * d);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.error_word = st->error_word;
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
     if (d == 64)
-        return kv4_block_rows(rows) == 8 ? launch_kv4_decode<64, 1>(p, stream) : launch_kv4_decode<64, 2>(p, stream);
-    return kv4_block_rows(rows) == 8 ? launch_kv4_decode<128, 1>(p, stream) : launch_kv4_decode<128, 2>(p, stream);
+        return kv4_block_rows(rows) == 8 ? launch_kv4_decode<64, 1>(p, plan, stream) : launch_kv4_decode<64, 2>(p, plan, stream);
+    return kv4_block_rows(rows) == 8 ? launch_kv4_decode<128, 1>(p, plan, stream) : launch_kv4_decode<128, 2>(p, plan, stream);
 }
 
 size_t fa_fp8_vt_bytes(int B, int H, int N, int d) {

@@ -66,24 +66,24 @@ struct Kv4DecodeParams {
 
 template <int D, int NT>
 struct Kv4DecCfg {
-    static constexpr int BN = NT == 1 ? 64 : 32;          // keys a tile
+    static constexpr int BN = 64;                         // keys a tile
     static constexpr int ROWS = 8 * NT;                   // query rows a warp
     static constexpr int WARPS = 4;                       // a CTA
-    static constexpr int MIN_CTAS = 3;                    // an SM
-    static constexpr int NK = NT == 1 ? 1 : 2;            // K stages of a warp's ring
-    static constexpr int NV = NT == 1 ? 1 : 2;            // V stages
+    static constexpr int MIN_CTAS = NT == 1 ? 3 : 2;      // an SM: 168 and 255 registers a thread
     static constexpr int MT = BN / 16;                    // mma key tiles
     static constexpr int ROWB = D / 2;                    // bytes of a row's codes
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
-    static constexpr int KSTAGE = TILE + 2 * WORDB;       // K codes, K words, V words
-    static constexpr int OFF_V = NK * KSTAGE;
-    static constexpr int OFF_SCALES = OFF_V + NV * TILE;
-    static constexpr int WARP_BYTES = OFF_SCALES + 2 * BN * 8;          // (scale, zero) of K and V last
-    static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][NK + NV]
-    static constexpr int OFF_MISC = OFF_BAR + WARPS * (NK + NV) * 8;
+    // a warp's shared memory: K codes, K words, V words; V codes; (scale, zero) of K and V
+    static constexpr int OFF_V = TILE + 2 * WORDB;
+    static constexpr int OFF_SCALES = OFF_V + TILE;
+    static constexpr int WARP_BYTES = OFF_SCALES + 2 * BN * 8;
+    static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][2]: K, V
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * 16;
     static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16;
-    static_assert(KSTAGE % 16 == 0 && TILE % 16 == 0 && WARP_BYTES % 16 == 0, "16-byte copies");
+    static constexpr int OSTRIDE = D + 4;                 // floats a row of a partial output in shared memory
+    static_assert(OFF_V % 16 == 0 && TILE % 16 == 0 && WARP_BYTES % 16 == 0, "16-byte copies");
+    static_assert(ROWS * (OSTRIDE + 2) * 4 <= WARP_BYTES, "a warp leaves its partial result in its memory");
 };
 
 __device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -126,13 +126,6 @@ constexpr float kNoRef = 3.4028234e38f;   // minus the reference before the firs
 // each half.
 __host__ __device__ constexpr int kv4_key(int m) { return m ^ ((m >> 1) & 1); }
 
-// ---------------------------------------------------------------- ranges --
-// The work is the sequence of all key tiles of all items, an item being a
-// (sequence, kv head, block of query rows) and `per` the items of a sequence.
-// Sequences differ in length, and only the device knows them, so the tiles are
-// cut into equal ranges, one a warp; a range's ends may lie inside an item,
-// which then has partial results: that of the item's first tiles in slot 1 of
-// their range, all others in slot 0 of theirs (a range has at most one each).
 struct Kv4Span {
     int nk, t0, n;      // used keys, first key tile and tiles of a sequence
 };
@@ -147,6 +140,538 @@ __device__ __forceinline__ Kv4Span kv4_span(const Kv4DecodeParams& p, int b) {
     return s;
 }
 
+// Row of [B * Nq * H] of query row r of kv head hk, and its place in lse.
+__device__ __forceinline__ size_t kv4_out_row(const Kv4DecodeParams& p, int b, int hk, int r, size_t& lse_at) {
+    const int i = r / p.G, h = hk * p.G + r - i * p.G;
+    lse_at = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
+    return (static_cast<size_t>(b) * p.Nq + i) * p.H + h;
+}
+
+// A query row's sum of partial results, held by a warp: D / 32 channels a
+// lane, the reference M (base 2) and the sum L.
+template <int D>
+struct Kv4Row {
+    float a[D / 32], M, L;
+    __device__ __forceinline__ Kv4Row() : M(-INFINITY), L(0.f) {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
+    }
+    // Adds the partial result with reference and sum `ml` and the lane's channels v.
+    __device__ __forceinline__ void take(float2 ml, const float* v) {
+        if (ml.x == -INFINITY && !isnan(ml.y)) return;      // no key of this row
+        const float m = fmaxf(M, ml.x);
+        const float w0 = M == -INFINITY ? 0.f : ex2(M - m), w1 = ex2(ml.x - m);
+        L = (M == -INFINITY ? L : L * w0) + ml.y * w1;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) a[e] = fmaf(v[e], w1, a[e] * w0);
+        M = m;
+    }
+    __device__ __forceinline__ void store(const Kv4DecodeParams& p, int b, int hk, int r) const {
+        const int lane = lane_id();
+        size_t lse_at;
+        const size_t row = kv4_out_row(p, b, hk, r, lse_at);
+        const bool some = !(L == 0.f);                      // a NaN sum stays NaN
+        const float inv = some ? 1.f / L : 0.f;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * (D / 32));
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16(a[2 * e] * inv, a[2 * e + 1] * inv);
+        if (lane == 0) p.lse[lse_at] = some ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+    }
+};
+
+// What a warp has of an item: O^T in mma fragments ([m][nt][mma row g8 / g8 + 8],
+// query rows 2 t4 + {0, 1}), the lane's sums of p and of p s^v z, minus the
+// reference (kNoRef: none), the exponent that O and za are scaled by.
+template <int D, int NT>
+struct Kv4Acc {
+    float2 o[D / 16][NT][2];
+    float2 l[NT], za[NT], nm[NT];
+    uint32_t ev;                    // biased exponent of the largest V scale
+};
+
+// One warp's attention over `count` key tiles (from tile `first` on) of kv head
+// hk of sequence b, for query rows r0 .. r0 + nrows - 1.  `ring` is the warp's
+// shared memory, bar_k its two barriers, `phase` their phase.  False when a
+// wait gave up.
+template <int D, int NT>
+__device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, NT>& acc, uint8_t* ring, uint64_t* bar_k,
+                                           uint32_t& phase, const WaitCtl& wc, int b, int hk, int r0, int nrows,
+                                           int nk, int first, int count) {
+    using C = Kv4DecCfg<D, NT>;
+    const int lane = lane_id(), g8 = lane >> 2, t4 = lane & 3;
+    const float kNegInf = -INFINITY;
+    uint64_t* bar_v = bar_k + 1;
+    float2* sck = reinterpret_cast<float2*>(ring + C::OFF_SCALES);
+    float2* scv = sck + C::BN;
+    const int qpos0 = nk - p.Nq;                             // key position of query 0
+    const int64_t row0 = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk + static_cast<int64_t>(first) * C::BN;
+    const int room = p.Nk - first * C::BN;
+    // loads of tile i: K with both words, and V (rows to be read are a multiple of 8)
+    auto load_k = [&](int i) {
+        if (lane == 0) {
+            const uint32_t rows = min(C::BN, room - i * C::BN);
+            const int64_t row = row0 + i * C::BN;
+            mbar_arrive_expect_tx(bar_k, rows * (C::ROWB + 4));
+            bulk_load(ring, p.codes[0] + row * C::ROWB, rows * C::ROWB, bar_k);
+            bulk_load(ring + C::TILE, p.words[0] + row, rows * 2, bar_k);
+            bulk_load(ring + C::TILE + C::WORDB, p.words[1] + row, rows * 2, bar_k);
+        }
+    };
+    auto load_v = [&](int i) {
+        if (lane == 0) {
+            const uint32_t rows = min(C::BN, room - i * C::BN);
+            mbar_arrive_expect_tx(bar_v, rows * C::ROWB);
+            bulk_load(ring + C::OFF_V, p.codes[1] + (row0 + i * C::BN) * C::ROWB, rows * C::ROWB, bar_v);
+        }
+    };
+    if (count > 0) {
+        load_k(0);
+        load_v(0);
+    }
+
+    // ------------------------------------- queries as B fragments --
+    // Row nt * 8 + g8, channels t4 * D/4 ..: of word w (8 codes), pair u of
+    // k-step pairs: codes (2u, 2u + 4) plain and (2u + 1, 2u + 5) times 1/16.
+    constexpr int W = D / 32;
+    uint32_t qf[NT][W][2][2];
+    float2 sq[NT], rf[NT];          // of rows nt * 8 + 2 t4 + {0, 1}: sum of q and the score factor
+    int hi[NT][2], lo[NT][2];       // their allowed keys are [lo, hi)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int rr = nt * 8 + g8;
+        uint4 raw[W];
+        const bool have = rr < nrows;
+        const int qi = (r0 + rr) / p.G;
+        const size_t qrow = have ? (static_cast<size_t>(b) * p.Nq + qi) * p.H + hk * p.G + (r0 + rr) - qi * p.G : 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            raw[w] = have ? *reinterpret_cast<const uint4*>(p.q + qrow * D + t4 * (D / 4) + w * 8) : make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;           // largest magnitude, as bf16 bits (NaN and infinity on top)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, (v[j] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(static_cast<int>(top >> 7), 14);             // biased exponent
+        const float qs = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f[8] = {bf16_lo(raw[w].x) * qs, bf16_hi(raw[w].x) * qs, bf16_lo(raw[w].y) * qs,
+                                bf16_hi(raw[w].y) * qs, bf16_lo(raw[w].z) * qs, bf16_hi(raw[w].z) * qs,
+                                bf16_lo(raw[w].w) * qs, bf16_hi(raw[w].w) * qs};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += f[j];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                qf[nt][w][u][0] = pack_f16(f[2 * u], f[2 * u + 4]);
+                qf[nt][w][u][1] = pack_f16(f[2 * u + 1] * 0.0625f, f[2 * u + 5] * 0.0625f);
+            }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= -5.9604644775390625e-8f;                                // -2^-24, as the codes
+        const float f = e >= 255 ? NAN : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
+        sq[nt].x = __shfl_sync(0xffffffffu, sum, 8 * t4);
+        sq[nt].y = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+        rf[nt].x = __shfl_sync(0xffffffffu, f, 8 * t4);
+        rf[nt].y = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int qp = qpos0 + (r0 + nt * 8 + 2 * t4 + j) / p.G;
+            hi[nt][j] = p.causal ? min(nk, qp + 1) : nk;
+            lo[nt][j] = p.window > 0 ? max(0, qp - p.window + 1) : 0;
+        }
+    }
+    const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
+
+    float2 (&oacc)[D / 16][NT][2] = acc.o;
+    float2 (&l)[NT] = acc.l, (&za)[NT] = acc.za, (&nm)[NT] = acc.nm;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) oacc[m][nt][0] = oacc[m][nt][1] = make_float2(0.f, 0.f);
+        l[nt] = za[nt] = make_float2(0.f, 0.f);
+        nm[nt] = make_float2(kNoRef, kNoRef);
+    }
+    uint32_t& ev = acc.ev;
+    ev = 6;
+    float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
+
+    for (int i = 0; i < count; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_k, phase, wc))) return false;
+        const uint8_t* st = ring;
+        const int k0 = (first + i) * C::BN;
+
+        // ---- scales and zeros: a key a lane
+        const bool edge = k0 + C::BN > nk;
+        {
+            const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + C::TILE);
+            uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
+#pragma unroll
+            for (int kk = 0; kk < C::BN / 32; ++kk) {
+                wk[kk] = ws[kk * 32 + lane];
+                wv[kk] = ws[C::BN + kk * 32 + lane];
+                top = max(top, wv[kk]);
+            }
+            top = __reduce_max_sync(0xffffffffu, top) >> 7;
+            if (edge || top >= 255u) {
+                // rows past the sequence may hold anything; a row whose V is
+                // NaN acts through its score
+                top = 0;
+#pragma unroll
+                for (int kk = 0; kk < C::BN / 32; ++kk) {
+                    if (wv[kk] >= 0x7f80u) {
+                        wk[kk] = kKv4NaN;
+                        wv[kk] = 0;
+                    }
+                    if (k0 + kk * 32 + lane >= nk) wv[kk] = 0;
+                    top = max(top, wv[kk]);
+                }
+                top = __reduce_max_sync(0xffffffffu, top) >> 7;
+            }
+            if (top > ev) {         // a larger scale than any before: O goes down with the new factor
+                const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    za[nt] = fmul2(za[nt], make_float2(d, d));
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], make_float2(d, d));
+                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], make_float2(d, d));
+                    }
+                }
+                ev = top;
+                vnorm = __uint_as_float((260u - ev) << 23);
+            }
+#pragma unroll
+            for (int kk = 0; kk < C::BN / 32; ++kk) {
+                sck[kk * 32 + lane] = make_float2(__uint_as_float((wk[kk] & 0xfff0u) << 16),
+                                                  __uint_as_float(0x4b000000u | (wk[kk] & 15u)) - 8388608.f);
+                scv[kk * 32 + lane] = make_float2(__uint_as_float((wv[kk] & 0xfff0u) << 16) * vnorm,
+                                                  __uint_as_float(0x4b000000u | (wv[kk] & 15u)) - 8388608.f);
+            }
+        }
+        __syncwarp();
+
+        // ---- scores, and p = 2^(x - reference).  A lane's sum over the tile tells
+        // when a score has passed the reference by so much that p s^v could
+        // leave fp16: then the scores are formed again (they are not kept), the
+        // reference moves to their maximum, and p is taken anew.
+        float2 e[C::MT][NT][2], ts[NT];
+        for (bool move = false;; move = true) {
+        float2 (&s)[C::MT][NT][2] = e;
+        // ---- S^T = C^k q^T: keys x 8 NT rows
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) {
+            uint32_t ka[W], kb[W];
+            const uint8_t* ra = st + (m * 16 + kv4_key(g8)) * C::ROWB + t4 * (W * 4);
+            const uint8_t* rb = ra + 8 * C::ROWB;
+            if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
+                ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+                kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(rb);
+                ka[0] = u.x; ka[1] = u.y;
+                kb[0] = v.x; kb[1] = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const uint32_t u = ka[w], v = kb[w], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (w == 0)
+                        mma_f16_first(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                      qf[nt][w][0][1]);
+                    else
+                        mma_f16(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                qf[nt][w][0][1]);
+                    mma_f16(s[m][nt], u8 & kNibLo, v8 & kNibLo, u8 & kNibHi, v8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
+                }
+            }
+        }
+        // ---- scores (over the row factor rf) and masks
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float2 sz = sck[m * 16 + half * 8 + kv4_key(g8)];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
+                                           make_float2(sz.x, sz.x));
+            }
+        if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int key = k0 + m * 16 + half * 8 + kv4_key(g8);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
+                        if (key >= hi[nt][1] || key < lo[nt][1]) s[m][nt][half].y = kNegInf;
+                    }
+                }
+        }
+
+        if (move) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 mx = s[0][nt][0];
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        mx.x = fmaxf(mx.x, s[m][nt][half].x);
+                        mx.y = fmaxf(mx.y, s[m][nt][half].y);
+                    }
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) {
+                    mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+                    mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+                }
+                // the reference never falls; -inf (nothing yet) leaves none
+                float2 n2 = fmul2(mx, make_float2(-rf[nt].x, -rf[nt].y));
+                n2 = make_float2(fminf(n2.x, nm[nt].x), fminf(n2.y, nm[nt].y));
+                const float2 a = make_float2(nm[nt].x == kNoRef ? 0.f : ex2(n2.x - nm[nt].x),
+                                             nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
+                nm[nt] = n2;
+                l[nt] = fmul2(l[nt], a);
+                za[nt] = fmul2(za[nt], a);
+#pragma unroll
+                for (int m = 0; m < D / 16; ++m) {
+                    oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
+                    oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
+                }
+            }
+        }
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ts[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
+                    e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
+                    ts[nt] = fadd2(ts[nt], e[m][nt][half]);
+                }
+            over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
+        }
+        if (move || !__any_sync(0xffffffffu, over)) break;
+        }
+        __syncwarp();               // K may be loaded again
+        if (i + 1 < count) load_k(i + 1);
+        // ---- p s^v as the B fragments of the second product
+        uint32_t pf[C::MT][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) l[nt] = fadd2(l[nt], ts[nt]);
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float2 sz = scv[m * 16 + half * 8 + kv4_key(g8)];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 w = fmul2(e[m][nt][half], make_float2(sz.x, sz.x));
+                    za[nt] = ffma2(w, make_float2(sz.y, sz.y), za[nt]);
+                    pf[m][nt][half] = transpose8x8(pack_f16(w.x, w.y));
+                }
+            }
+        // ---- O^T += C^v (p s^v)^T
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_v, phase, wc))) return false;
+        const uint8_t* sv = ring + C::OFF_V;
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) {
+            constexpr int VW = D / 64;                 // words of codes a lane and key
+            uint32_t v[4][VW];                         // mma indices 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const int row = m * 16 + (kk >> 1) * 8 + kv4_key(2 * t4 + (kk & 1));
+                const uint8_t* src = sv + row * C::ROWB + g8 * (VW * 4);
+                if constexpr (D == 128) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(src);
+                    v[kk][0] = u.x;
+                    v[kk][VW - 1] = u.y;
+                } else {
+                    v[kk][0] = *reinterpret_cast<const uint32_t*>(src);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int up = 0; up < 2; ++up) {       // codes 0-3, then 4-7 of the word
+                    const uint32_t sel = up ? 0x7632u : 0x5410u;
+                    const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
+                    const uint32_t u8 = u >> 8, y8 = y >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(oacc[w * 4 + up * 2][nt], u & kNibLo, u & kNibHi, y & kNibLo, y & kNibHi,
+                                pf[m][nt][0], pf[m][nt][1]);
+                        mma_f16(oacc[w * 4 + up * 2 + 1][nt], u8 & kNibLo, u8 & kNibHi, y8 & kNibLo, y8 & kNibHi,
+                                pf[m][nt][0], pf[m][nt][1]);
+                    }
+                }
+        }
+        __syncwarp();               // and V
+        if (i + 1 < count) load_v(i + 1);
+        phase ^= 1;
+    }
+
+    return true;
+}
+
+// Hands each of the warp's query rows to put(row, channels from g8 * D/8 on,
+// reference, sum): a lane of each g8 has D/8 channels of two rows of each nt.
+// O is left as it is (relative to the reference).
+template <int D, int NT, typename Put>
+__device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, int nrows, const Put& put) {
+    const int t4 = lane_id() & 3;
+    const float back = ldexpf(1.f, static_cast<int>(acc.ev) - 133);       // undoes vnorm
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+            acc.l[nt].x += __shfl_xor_sync(0xffffffffu, acc.l[nt].x, o);
+            acc.l[nt].y += __shfl_xor_sync(0xffffffffu, acc.l[nt].y, o);
+            acc.za[nt].x += __shfl_xor_sync(0xffffffffu, acc.za[nt].x, o);
+            acc.za[nt].y += __shfl_xor_sync(0xffffffffu, acc.za[nt].y, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = nt * 8 + 2 * t4 + j;
+            if (r >= nrows) continue;
+            const float z = j ? acc.za[nt].y : acc.za[nt].x, n1 = j ? acc.nm[nt].y : acc.nm[nt].x;
+            float a[D / 8];
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {      // codes times 2^-24, and 2^-20
+                a[2 * m] = fmaf(j ? acc.o[m][nt][0].y : acc.o[m][nt][0].x, 16777216.f, -z) * back;
+                a[2 * m + 1] = fmaf(j ? acc.o[m][nt][1].y : acc.o[m][nt][1].x, 1048576.f, -z) * back;
+            }
+            put(r, a, n1 == kNoRef ? -INFINITY : -n1, j ? acc.l[nt].y : acc.l[nt].x);
+        }
+    }
+}
+
+// After a wait that gave up: lets the copies in flight land before the CTA exits.
+__device__ __forceinline__ void kv4_drain(uint64_t* bar_k, uint32_t phase, int* error_word) {
+    if (lane_id() == 0) {
+        volatile int no_abort = 0;
+        const WaitCtl dw{&no_abort, error_word, 200000000ull};
+        mbar_wait(bar_k, phase, dw);
+        mbar_wait(bar_k, phase ^ 1, dw);        // the next tile's K, where V gave up
+        mbar_wait(bar_k + 1, phase, dw);
+    }
+}
+
+// ------------------------------------------------ few tiles: a cluster an item --
+// An item (sequence, kv head, block of query rows) to each cluster of CTAs, its
+// tiles in equal parts to the warps of the cluster.  The warps of a CTA put
+// their results together in shared memory, the CTAs in distributed shared
+// memory: no second kernel and no workspace.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 4 bytes of the shared memory of the cluster's CTA `rank`, at this CTA's address `p`.
+__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Kv4DecCfg<D, NT>::WARPS * 32, Kv4DecCfg<D, NT>::MIN_CTAS)
+kv4_cluster_kernel(const Kv4DecodeParams p) {
+    using C = Kv4DecCfg<D, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = lane_id(), g8 = lane >> 2;
+    const int ctas = cluster_size(), rank = cluster_rank();
+    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * 2;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+    if (lane == 0) {
+        mbar_init(bar_k, 1);
+        mbar_init(bar_k + 1, 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 0) *abort_flag = 0;
+    const int per = p.Hkv * p.row_blocks;
+    const int id = blockIdx.x / ctas;
+    const int b = id / per, item = id - b * per, hk = item / p.row_blocks;
+    const int r0 = (item - hk * p.row_blocks) * C::ROWS, nrows = min(C::ROWS, p.Nq * p.G - r0);
+    const Kv4Span sp = kv4_span<C::BN>(p, b);
+    const int all = ctas * C::WARPS, me = rank * C::WARPS + warp;
+    const int t0 = static_cast<int>(static_cast<int64_t>(sp.n) * me / all);
+    const int t1 = static_cast<int>(static_cast<int64_t>(sp.n) * (me + 1) / all);
+    __syncthreads();
+    const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
+    uint32_t phase = 0;
+    Kv4Acc<D, NT> acc;
+    const bool ok = kv4_attend<D, NT>(p, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
+                                      sp.t0 + t0, t1 - t0);
+    if (!ok) kv4_drain(bar_k, phase, p.error_word);
+    auto partial = [&](int w) { return reinterpret_cast<float*>(smem + w * C::WARP_BYTES); };   // [ROWS][OSTRIDE]
+    auto stats = [&](int w) { return partial(w) + C::ROWS * C::OSTRIDE; };                      // [ROWS][2]
+    kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float m, float l) {
+        float4* dst = reinterpret_cast<float4*>(partial(warp) + r * C::OSTRIDE + g8 * (D / 8));
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+        if (g8 == 0) *reinterpret_cast<float2*>(stats(warp) + 2 * r) = make_float2(m, l);
+    });
+    __syncthreads();
+    constexpr int V = D / 32;
+    for (int r = warp; r < nrows; r += C::WARPS) {
+        Kv4Row<D> sum;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w)
+            sum.take(make_float2(stats(w)[2 * r], stats(w)[2 * r + 1]), partial(w) + r * C::OSTRIDE + lane * V);
+        if (ctas == 1) {
+            sum.store(p, b, hk, r0 + r);
+        } else {            // over warp 0's row, which no other warp reads
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < V; ++e) partial(0)[r * C::OSTRIDE + lane * V + e] = sum.a[e];
+            if (lane == 0) *reinterpret_cast<float2*>(stats(0) + 2 * r) = make_float2(sum.M, sum.L);
+        }
+    }
+    if (ctas == 1) return;
+    cluster_barrier();
+    for (int r = me; r < nrows; r += all) {
+        Kv4Row<D> sum;
+        for (int c = 0; c < ctas; ++c) {
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = cluster_load(partial(0) + r * C::OSTRIDE + lane * V + e, c);
+            sum.take(make_float2(cluster_load(stats(0) + 2 * r, c), cluster_load(stats(0) + 2 * r + 1, c)), v);
+        }
+        sum.store(p, b, hk, r0 + r);
+    }
+    cluster_barrier();      // the CTAs' memory stays until all have read it
+}
+
+// ------------------------------------------------------ many tiles: ranges --
+// The work is the sequence of all key tiles of all items, `per` items to a
+// sequence.  Sequences differ in length, and only the device knows them, so the
+// tiles are cut into equal ranges, one a warp; a range's ends may lie inside an
+// item, which then has partial results: that of the item's first tiles in slot 1
+// of their range, all others in slot 0 of theirs (a range has at most one each).
 // The cut of `total` tiles (below 2^31) into ranges of q or, the first rem,
 // q + 1 tiles; fewer ranges than p.ranges when there are fewer tiles.
 struct Kv4Cut {
@@ -163,13 +688,6 @@ struct Kv4Cut {
     }
 };
 
-// Row of [B * Nq * H] of query row r of kv head hk, and its place in lse.
-__device__ __forceinline__ size_t kv4_out_row(const Kv4DecodeParams& p, int b, int hk, int r, size_t& lse_at) {
-    const int i = r / p.G, h = hk * p.G + r - i * p.G;
-    lse_at = (static_cast<size_t>(b) * p.H + h) * p.Nq + i;
-    return (static_cast<size_t>(b) * p.Nq + i) * p.H + h;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4DecCfg<D, NT>::WARPS * 32, Kv4DecCfg<D, NT>::MIN_CTAS)
 kv4_decode_kernel(const Kv4DecodeParams p) {
@@ -177,18 +695,16 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     // the merge launched after this grid may be scheduled now
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(128) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = lane_id();
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const float kNegInf = -INFINITY;
+    const int warp = threadIdx.x >> 5, lane = lane_id(), g8 = lane >> 2;
     const int per = p.Hkv * p.row_blocks;
-    uint64_t* kbar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * (C::NK + C::NV);
-    uint64_t* vbar = kbar + C::NK;
+    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * 2;
     int* sh_b = reinterpret_cast<int*>(smem + C::OFF_MISC);
     int* sh_base = sh_b + C::WARPS;
     int* sh_sum = sh_base + C::WARPS;
     volatile int* abort_flag = sh_sum + C::WARPS;
     if (lane == 0) {
-        for (int s = 0; s < C::NK + C::NV; ++s) mbar_init(kbar + s, 1);
+        mbar_init(bar_k, 1);
+        mbar_init(bar_k + 1, 1);
         fence_barrier_init();
     }
     if (threadIdx.x == 0) *abort_flag = 0;
@@ -241,14 +757,8 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     int b = sh_b[warp];
     int base = sh_base[warp];
     const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
-    uint8_t* ring = smem + warp * C::WARP_BYTES;
-    float2* sck = reinterpret_cast<float2*>(ring + C::OFF_SCALES);
-    float2* scv = sck + C::BN;
-    uint32_t ks = 0, kp = 0, vs = 0, vp = 0;        // ring stage and phase of K and V, over all segments
-    bool ok = true;
-
-    while (x < x_end && ok) {
-        // ------------------------------------------------- a segment --
+    uint32_t phase = 0;
+    while (x < x_end) {
         const Kv4Span sp = kv4_span<C::BN>(p, b);
         if (sp.n == 0) {
             ++b;
@@ -258,402 +768,38 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         const int tile0 = x - base - item * sp.n;
         const int count = min(sp.n - tile0, x_end - x);
         const int hk = item / p.row_blocks;
-        const int r0 = (item - hk * p.row_blocks) * C::ROWS;     // first of the query rows
-        const int nrows = min(C::ROWS, p.Nq * p.G - r0);
-        const int nk = sp.nk, qpos0 = nk - p.Nq;                 // key position of query 0
-
-        const int first = sp.t0 + tile0;
-        const int64_t row0 = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk + static_cast<int64_t>(first) * C::BN;
-        const int room = p.Nk - first * C::BN;
-        // loads of the segment's tile i: K with both words, and V (rows to be
-        // read are a multiple of 8)
-        auto load_k = [&](int i, uint32_t stage) {
-            if (lane == 0) {
-                const uint32_t rows = min(C::BN, room - i * C::BN);
-                const int64_t row = row0 + i * C::BN;
-                uint8_t* dst = ring + stage * C::KSTAGE;
-                mbar_arrive_expect_tx(kbar + stage, rows * (C::ROWB + 4));
-                bulk_load(dst, p.codes[0] + row * C::ROWB, rows * C::ROWB, kbar + stage);
-                bulk_load(dst + C::TILE, p.words[0] + row, rows * 2, kbar + stage);
-                bulk_load(dst + C::TILE + C::WORDB, p.words[1] + row, rows * 2, kbar + stage);
-            }
-        };
-        auto load_v = [&](int i, uint32_t stage) {
-            if (lane == 0) {
-                const uint32_t rows = min(C::BN, room - i * C::BN);
-                mbar_arrive_expect_tx(vbar + stage, rows * C::ROWB);
-                bulk_load(ring + C::OFF_V + stage * C::TILE, p.codes[1] + (row0 + i * C::BN) * C::ROWB, rows * C::ROWB,
-                          vbar + stage);
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < C::NK; ++i)
-            if (i < count) load_k(i, ks + i < C::NK ? ks + i : ks + i - C::NK);
-#pragma unroll
-        for (int i = 0; i < C::NV; ++i)
-            if (i < count) load_v(i, vs + i < C::NV ? vs + i : vs + i - C::NV);
-
-        // ------------------------------------- queries as B fragments --
-        // Row nt * 8 + g8, channels t4 * D/4 ..: of word w (8 codes), pair u of
-        // k-step pairs: codes (2u, 2u + 4) plain and (2u + 1, 2u + 5) times 1/16.
-        constexpr int W = D / 32;
-        uint32_t qf[NT][W][2][2];
-        float2 sq[NT], rf[NT];          // of rows nt * 8 + 2 t4 + {0, 1}: sum of q and the score factor
-        int hi[NT][2], lo[NT][2];       // their allowed keys are [lo, hi)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int rr = nt * 8 + g8;
-            uint4 raw[W];
-            const bool have = rr < nrows;
-            const int qi = (r0 + rr) / p.G;
-            const size_t qrow = have ? (static_cast<size_t>(b) * p.Nq + qi) * p.H + hk * p.G + (r0 + rr) - qi * p.G : 0;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                raw[w] = have ? *reinterpret_cast<const uint4*>(p.q + qrow * D + t4 * (D / 4) + w * 8) : make_uint4(0, 0, 0, 0);
-            uint32_t top = 0;           // largest magnitude, as bf16 bits (NaN and infinity on top)
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7fffu, (v[j] >> 16) & 0x7fffu));
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = max(static_cast<int>(top >> 7), 14);             // biased exponent
-            const float qs = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f[8] = {bf16_lo(raw[w].x) * qs, bf16_hi(raw[w].x) * qs, bf16_lo(raw[w].y) * qs,
-                                    bf16_hi(raw[w].y) * qs, bf16_lo(raw[w].z) * qs, bf16_hi(raw[w].z) * qs,
-                                    bf16_lo(raw[w].w) * qs, bf16_hi(raw[w].w) * qs};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum += f[j];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    qf[nt][w][u][0] = pack_f16(f[2 * u], f[2 * u + 4]);
-                    qf[nt][w][u][1] = pack_f16(f[2 * u + 1] * 0.0625f, f[2 * u + 5] * 0.0625f);
-                }
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum *= -5.9604644775390625e-8f;                                // -2^-24, as the codes
-            const float f = e >= 255 ? NAN : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
-            sq[nt].x = __shfl_sync(0xffffffffu, sum, 8 * t4);
-            sq[nt].y = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
-            rf[nt].x = __shfl_sync(0xffffffffu, f, 8 * t4);
-            rf[nt].y = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int qp = qpos0 + (r0 + nt * 8 + 2 * t4 + j) / p.G;
-                hi[nt][j] = p.causal ? min(nk, qp + 1) : nk;
-                lo[nt][j] = p.window > 0 ? max(0, qp - p.window + 1) : 0;
-            }
+        const int r0 = (item - hk * p.row_blocks) * C::ROWS, nrows = min(C::ROWS, p.Nq * p.G - r0);
+        Kv4Acc<D, NT> acc;
+        if (!kv4_attend<D, NT>(p, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
+                               sp.t0 + tile0, count)) {
+            kv4_drain(bar_k, phase, p.error_word);
+            return;
         }
-        const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
-
-        float2 oacc[D / 16][NT][2];     // [m][nt][row g8 / g8 + 8 of the mma], rows 2 t4 + {0, 1}
-        float2 l[NT], za[NT], nm[NT];   // sums of p and of p s^v z, minus the reference (kNoRef: none yet)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) oacc[m][nt][0] = oacc[m][nt][1] = make_float2(0.f, 0.f);
-            l[nt] = za[nt] = make_float2(0.f, 0.f);
-            nm[nt] = make_float2(kNoRef, kNoRef);
-        }
-        uint32_t ev = 6;                // biased exponent of the largest V scale so far
-        float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
-
-        for (int i = 0; i < count; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(kbar + ks, kp, wc))) { ok = false; break; }
-            const uint8_t* st = ring + ks * C::KSTAGE;
-            const int k0 = (first + i) * C::BN;
-
-            // ---- scales and zeros: a key a lane
-            const bool edge = k0 + C::BN > nk;
-            {
-                const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + C::TILE);
-                uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
-#pragma unroll
-                for (int kk = 0; kk < C::BN / 32; ++kk) {
-                    wk[kk] = ws[kk * 32 + lane];
-                    wv[kk] = ws[C::BN + kk * 32 + lane];
-                    top = max(top, wv[kk]);
-                }
-                top = __reduce_max_sync(0xffffffffu, top) >> 7;
-                if (edge || top >= 255u) {
-                    // rows past the sequence may hold anything; a row whose V is
-                    // NaN acts through its score
-                    top = 0;
-#pragma unroll
-                    for (int kk = 0; kk < C::BN / 32; ++kk) {
-                        if (wv[kk] >= 0x7f80u) {
-                            wk[kk] = kKv4NaN;
-                            wv[kk] = 0;
-                        }
-                        if (k0 + kk * 32 + lane >= nk) wv[kk] = 0;
-                        top = max(top, wv[kk]);
-                    }
-                    top = __reduce_max_sync(0xffffffffu, top) >> 7;
-                }
-                if (top > ev) {         // a larger scale than any before: O goes down with the new factor
-                    const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        za[nt] = fmul2(za[nt], make_float2(d, d));
-#pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            oacc[m][nt][0] = fmul2(oacc[m][nt][0], make_float2(d, d));
-                            oacc[m][nt][1] = fmul2(oacc[m][nt][1], make_float2(d, d));
-                        }
-                    }
-                    ev = top;
-                    vnorm = __uint_as_float((260u - ev) << 23);
-                }
-#pragma unroll
-                for (int kk = 0; kk < C::BN / 32; ++kk) {
-                    sck[kk * 32 + lane] = make_float2(__uint_as_float((wk[kk] & 0xfff0u) << 16),
-                                                      __uint_as_float(0x4b000000u | (wk[kk] & 15u)) - 8388608.f);
-                    scv[kk * 32 + lane] = make_float2(__uint_as_float((wv[kk] & 0xfff0u) << 16) * vnorm,
-                                                      __uint_as_float(0x4b000000u | (wv[kk] & 15u)) - 8388608.f);
-                }
-            }
-            __syncwarp();
-
-            // ---- scores, and p = 2^(x - reference).  A lane's sum over the tile tells
-            // when a score has passed the reference by so much that p s^v could
-            // leave fp16: then the scores are formed again (they are not kept), the
-            // reference moves to their maximum, and p is taken anew.
-            float2 e[C::MT][NT][2], ts[NT];
-            for (bool move = false;; move = true) {
-            float2 (&s)[C::MT][NT][2] = e;
-            // ---- S^T = C^k q^T: keys x 8 NT rows
-#pragma unroll
-            for (int m = 0; m < C::MT; ++m) {
-                uint32_t ka[W], kb[W];
-                const uint8_t* ra = st + (m * 16 + kv4_key(g8)) * C::ROWB + t4 * (W * 4);
-                const uint8_t* rb = ra + 8 * C::ROWB;
-                if constexpr (D == 128) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
-                    ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
-                    kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(rb);
-                    ka[0] = u.x; ka[1] = u.y;
-                    kb[0] = v.x; kb[1] = v.y;
-                }
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const uint32_t u = ka[w], v = kb[w], u8 = u >> 8, v8 = v >> 8;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (w == 0)
-                            mma_f16_first(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
-                                          qf[nt][w][0][1]);
-                        else
-                            mma_f16(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
-                                    qf[nt][w][0][1]);
-                        mma_f16(s[m][nt], u8 & kNibLo, v8 & kNibLo, u8 & kNibHi, v8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
-                    }
-                }
-            }
-            // ---- scores (over the row factor rf) and masks
-#pragma unroll
-            for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float2 sz = sck[m * 16 + half * 8 + kv4_key(g8)];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
-                                               make_float2(sz.x, sz.x));
-                }
-            if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
-#pragma unroll
-                for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int key = k0 + m * 16 + half * 8 + kv4_key(g8);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
-                            if (key >= hi[nt][1] || key < lo[nt][1]) s[m][nt][half].y = kNegInf;
-                        }
-                    }
-            }
-
-            if (move) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float2 mx = s[0][nt][0];
-#pragma unroll
-                    for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            mx.x = fmaxf(mx.x, s[m][nt][half].x);
-                            mx.y = fmaxf(mx.y, s[m][nt][half].y);
-                        }
-#pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) {
-                        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
-                        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
-                    }
-                    // the reference never falls; -inf (nothing yet) leaves none
-                    float2 n2 = fmul2(mx, make_float2(-rf[nt].x, -rf[nt].y));
-                    n2 = make_float2(fminf(n2.x, nm[nt].x), fminf(n2.y, nm[nt].y));
-                    const float2 a = make_float2(nm[nt].x == kNoRef ? 0.f : ex2(n2.x - nm[nt].x),
-                                                 nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
-                    nm[nt] = n2;
-                    l[nt] = fmul2(l[nt], a);
-                    za[nt] = fmul2(za[nt], a);
-#pragma unroll
-                    for (int m = 0; m < D / 16; ++m) {
-                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
-                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
-                    }
-                }
-            }
-            bool over = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                ts[nt] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
-                        e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
-                        ts[nt] = fadd2(ts[nt], e[m][nt][half]);
-                    }
-                over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
-            }
-            if (move || !__any_sync(0xffffffffu, over)) break;
-            }
-            __syncwarp();               // this K stage may be loaded again
-            if (i + C::NK < count) load_k(i + C::NK, ks);
-            ks = ks + 1 == C::NK ? 0 : ks + 1;
-            kp ^= ks == 0;
-            // ---- p s^v as the B fragments of the second product
-            uint32_t pf[C::MT][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) l[nt] = fadd2(l[nt], ts[nt]);
-#pragma unroll
-            for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float2 sz = scv[m * 16 + half * 8 + kv4_key(g8)];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float2 w = fmul2(e[m][nt][half], make_float2(sz.x, sz.x));
-                        za[nt] = ffma2(w, make_float2(sz.y, sz.y), za[nt]);
-                        pf[m][nt][half] = transpose8x8(pack_f16(w.x, w.y));
-                    }
-                }
-            // ---- O^T += C^v (p s^v)^T
-            if (!__all_sync(0xffffffffu, mbar_wait(vbar + vs, vp, wc))) { ok = false; break; }
-            const uint8_t* sv = ring + C::OFF_V + vs * C::TILE;
-#pragma unroll
-            for (int m = 0; m < C::MT; ++m) {
-                constexpr int VW = D / 64;                 // words of codes a lane and key
-                uint32_t v[4][VW];                         // mma indices 2t, 2t+1, 2t+8, 2t+9
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const int row = m * 16 + (kk >> 1) * 8 + kv4_key(2 * t4 + (kk & 1));
-                    const uint8_t* src = sv + row * C::ROWB + g8 * (VW * 4);
-                    if constexpr (D == 128) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(src);
-                        v[kk][0] = u.x;
-                        v[kk][VW - 1] = u.y;
-                    } else {
-                        v[kk][0] = *reinterpret_cast<const uint32_t*>(src);
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < VW; ++w)
-#pragma unroll
-                    for (int up = 0; up < 2; ++up) {       // codes 0-3, then 4-7 of the word
-                        const uint32_t sel = up ? 0x7632u : 0x5410u;
-                        const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-                        const uint32_t u8 = u >> 8, y8 = y >> 8;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(oacc[w * 4 + up * 2][nt], u & kNibLo, u & kNibHi, y & kNibLo, y & kNibHi,
-                                    pf[m][nt][0], pf[m][nt][1]);
-                            mma_f16(oacc[w * 4 + up * 2 + 1][nt], u8 & kNibLo, u8 & kNibHi, y8 & kNibLo, y8 & kNibHi,
-                                    pf[m][nt][0], pf[m][nt][1]);
-                        }
-                    }
-            }
-            __syncwarp();               // this V stage may be loaded again
-            if (i + C::NV < count) load_v(i + C::NV, vs);
-            vs = vs + 1 == C::NV ? 0 : vs + 1;
-            vp ^= vs == 0;
-        }
-
-        // ------------------------------------------------- its result --
-        // Lane (g8, t4) holds channels g8 * D/8 .. of rows nt * 8 + 2 t4 + {0, 1}.
         const bool whole = count == sp.n;
-        const float back = ldexpf(1.f, static_cast<int>(ev) - 133);       // undoes vnorm
+        kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float m, float l) {
+            if (whole) {
+                const bool some = !(l == 0.f);      // a NaN sum stays NaN
+                const float inv = some ? 1.f / l : 0.f;
+                size_t lse_at;
+                const size_t row = kv4_out_row(p, b, hk, r0 + r, lse_at);
+                uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + g8 * (D / 8));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+                for (int v = 0; v < D / 64; ++v)
+                    dst[v] = make_uint4(pack_bf16(a[8 * v] * inv, a[8 * v + 1] * inv), pack_bf16(a[8 * v + 2] * inv, a[8 * v + 3] * inv),
+                                        pack_bf16(a[8 * v + 4] * inv, a[8 * v + 5] * inv), pack_bf16(a[8 * v + 6] * inv, a[8 * v + 7] * inv));
+                if (g8 == 0) p.lse[lse_at] = some ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                const size_t at_row = (static_cast<size_t>(range) * 2 + (tile0 == 0)) * C::ROWS + r;
+                float4* dst = reinterpret_cast<float4*>(p.o_part + at_row * D + g8 * (D / 8));
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                l[nt].x += __shfl_xor_sync(0xffffffffu, l[nt].x, o);
-                l[nt].y += __shfl_xor_sync(0xffffffffu, l[nt].y, o);
-                za[nt].x += __shfl_xor_sync(0xffffffffu, za[nt].x, o);
-                za[nt].y += __shfl_xor_sync(0xffffffffu, za[nt].y, o);
+                for (int v = 0; v < D / 32; ++v) dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+                if (g8 == 0) p.ml_part[at_row] = make_float2(m, l);
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = nt * 8 + 2 * t4 + j;
-                if (r >= nrows) continue;
-                const float L = j ? l[nt].y : l[nt].x, z = j ? za[nt].y : za[nt].x, n1 = j ? nm[nt].y : nm[nt].x;
-                const bool some = !(L == 0.f);      // a NaN sum stays NaN
-                const float f = whole ? (some ? back / L : 0.f) : back;
-                float a[D / 8];
-#pragma unroll
-                for (int m = 0; m < D / 16; ++m) {  // codes times 2^-24, and 2^-20
-                    a[2 * m] = fmaf(j ? oacc[m][nt][0].y : oacc[m][nt][0].x, 16777216.f, -z) * f;
-                    a[2 * m + 1] = fmaf(j ? oacc[m][nt][1].y : oacc[m][nt][1].x, 1048576.f, -z) * f;
-                }
-                if (whole) {
-                    size_t lse_at;
-                    const size_t row = kv4_out_row(p, b, hk, r0 + r, lse_at);
-                    uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + g8 * (D / 8));
-#pragma unroll
-                    for (int v = 0; v < D / 64; ++v)
-                        dst[v] = make_uint4(pack_bf16(a[8 * v], a[8 * v + 1]), pack_bf16(a[8 * v + 2], a[8 * v + 3]),
-                                            pack_bf16(a[8 * v + 4], a[8 * v + 5]), pack_bf16(a[8 * v + 6], a[8 * v + 7]));
-                    if (g8 == 0) p.lse[lse_at] = some ? (__log2f(L) - n1) * 0.6931471805599453f : -INFINITY;
-                } else {
-                    const size_t at_row = (static_cast<size_t>(range) * 2 + (tile0 == 0)) * C::ROWS + r;
-                    float4* dst = reinterpret_cast<float4*>(p.o_part + at_row * D + g8 * (D / 8));
-#pragma unroll
-                    for (int v = 0; v < D / 32; ++v)
-                        dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
-                    if (g8 == 0) p.ml_part[at_row] = make_float2(n1 == kNoRef ? kNegInf : -n1, L);
-                }
-            }
-        }
+        });
         x += count;
         if (x - base == sp.n * per) {
             base = x;
             ++b;
-        }
-    }
-    if (!ok && lane == 0) {
-        // let the copies in flight land before the CTA exits
-        volatile int no_abort = 0;
-        const WaitCtl dw{&no_abort, p.error_word, 200000000ull};
-        for (int s = 0; s < C::NK; ++s) {
-            mbar_wait(kbar + ks, kp, dw);
-            ks = ks + 1 == C::NK ? 0 : ks + 1;
-            kp ^= ks == 0;
-        }
-        for (int s = 0; s < C::NV; ++s) {
-            mbar_wait(vbar + vs, vp, dw);
-            vs = vs + 1 == C::NV ? 0 : vs + 1;
-            vp ^= vs == 0;
         }
     }
 }
@@ -694,19 +840,7 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
     // end before that one.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > 0 && c0 == c1) return;              // written by the range's own warp
-    float a[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) a[e] = 0.f;
-    float M = -INFINITY, L = 0.f;
-    auto take = [&](float m, float sum, const float (&v)[V]) {
-        if (m == -INFINITY && !isnan(sum)) return;      // no key of this row
-        const float m_new = fmaxf(M, m);
-        const float w0 = M == -INFINITY ? 0.f : ex2(M - m_new), w1 = ex2(m - m_new);
-        L = (M == -INFINITY ? L : L * w0) + sum * w1;
-#pragma unroll
-        for (int e = 0; e < V; ++e) a[e] = fmaf(v[e], w1, a[e] * w0);
-        M = m_new;
-    };
+    Kv4Row<D> sum;
     if (n > 0) {
         auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0)) * C::ROWS + r % C::ROWS; };
         for (int c = c0 + warp; c <= c1; c += AHEAD * warps) {
@@ -720,31 +854,19 @@ kv4_merge_kernel(const Kv4DecodeParams p) {
                 for (int e = 0; e < V; ++e) v[i][e] = p.o_part[from * D + lane * V + e];
             }
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) take(ml[i].x, ml[i].y, v[i]);
+            for (int i = 0; i < AHEAD; ++i) sum.take(ml[i], v[i]);
         }
         const int used = min(warps, c1 - c0 + 1);
 #pragma unroll
-        for (int e = 0; e < V; ++e) sm_a[warp][lane * V + e] = a[e];
-        if (lane == 0) sm_ml[warp] = make_float2(M, L);
+        for (int e = 0; e < V; ++e) sm_a[warp][lane * V + e] = sum.a[e];
+        if (lane == 0) sm_ml[warp] = make_float2(sum.M, sum.L);
         __syncthreads();
         if (warp != 0) return;
-        for (int w = 1; w < used; ++w) {
-            float v[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = sm_a[w][lane * V + e];
-            take(sm_ml[w].x, sm_ml[w].y, v);
-        }
+        for (int w = 1; w < used; ++w) sum.take(sm_ml[w], &sm_a[w][lane * V]);
     } else if (warp != 0) {
         return;
     }
-    size_t lse_at;
-    const size_t row = kv4_out_row(p, b, hk, r, lse_at);
-    const bool some = !(L == 0.f);              // a NaN sum stays NaN
-    const float inv = some ? 1.f / L : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * V);
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16(a[2 * e] * inv, a[2 * e + 1] * inv);
-    if (lane == 0) p.lse[lse_at] = some ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+    sum.store(p, b, hk, r);
 }
 
 }  // namespace fa

@@ -70,16 +70,18 @@ def test_sizes():
         return (n + 255) // 256 * 256
 
     size = fa.fa_fwd_kv4_workspace_size
-    assert size(2, 8, 2, 1, 512, 128, 1) == up(2 * (2 * 2) * 8 * 130 * 4)
-    assert size(2, 8, 2, 1, 512, 128, 4) == up(2 * (4 * 2 * 2) * 8 * 130 * 4)
-    assert size(2, 8, 2, 3, 512, 64, 4) == up(2 * (4 * 2 * 2) * 16 * 66 * 4)
-    assert size(2, 8, 2, 7, 512, 64, 3) == up(2 * (3 * 2 * 2 * 2) * 16 * 66 * 4)
+    assert size(2, 8, 2, 1, 512, 128, 0, 1) == up(2 * (2 * 2) * 8 * 130 * 4)
+    assert size(2, 8, 2, 1, 512, 128, 0, 4) == up(2 * (4 * 2 * 2) * 8 * 130 * 4)
+    assert size(2, 8, 2, 3, 512, 64, 0, 4) == up(2 * (4 * 2 * 2) * 16 * 66 * 4)
+    assert size(2, 8, 2, 7, 512, 64, 0, 3) == up(2 * (3 * 2 * 2 * 2) * 16 * 66 * 4)
     back = 2 * (2 * 512 * 2 * 128 * 2)
-    assert size(2, 8, 2, 500, 512, 128, 1) == back
-    assert size(2, 8, 2, 500, 512, 128, 3) == back + up(3 * 2 * 500 * 8 * 129 * 4)
-    assert size(2, 8, 2, 1, 512, 128, 0) >= 0 and size(2, 8, 2, 500, 512, 128, 0) >= back
-    assert size(2, 8, 3, 1, 512, 128, 4) == 0       # 8 heads over 3: refused
-    assert size(0, 8, 2, 1, 512, 128, 4) == 0 and size(2, 8, 2, 1, 512, 128, -1) == 0
+    assert size(2, 8, 2, 500, 512, 128, 0, 1) == back
+    assert size(2, 8, 2, 500, 512, 128, 0, 3) == back + up(3 * 2 * 500 * 8 * 129 * 4)
+    assert size(2, 8, 2, 1, 512, 128, 0, 0) == 0 and size(1, 8, 8, 1, 65536, 128, 0, 0) > 0
+    assert size(1, 8, 8, 1, 65536, 128, 100, 0) == 0        # a window leaves few tiles: one kernel
+    assert size(2, 8, 2, 1, 512, 128, 0, 0) >= 0 and size(2, 8, 2, 500, 512, 128, 0, 0) >= back
+    assert size(2, 8, 3, 1, 512, 128, 0, 4) == 0       # 8 heads over 3: refused
+    assert size(0, 8, 2, 1, 512, 128, 0, 4) == 0 and size(2, 8, 2, 1, 512, 128, 0, -1) == 0
 
 
 # ------------------------------------------------------------- the binding --

@@ -519,7 +519,7 @@ def test_step_in_a_graph_on_a_side_stream(Nq):
                   q=queries(B, Nq, H, d, seed + 3), starts=torch.tensor([100, 700], dtype=torch.int32, device=DEV))
         st["lens"] = st["starts"] + Nq
         ns = 4
-        st["ws"] = torch.empty(fa.fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, ns), dtype=torch.uint8, device=DEV)
+        st["ws"] = torch.empty(fa.fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, 0, ns), dtype=torch.uint8, device=DEV)
         st["o"], st["lse"] = torch.empty_like(st["q"]), torch.empty((B, H, Nq), device=DEV)
 
         def step(st=st, ns=ns):
