@@ -232,6 +232,24 @@ int make_map_u8_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+// Tensor map over the V codes of a 4-bit cache, [heads, rows, row_bytes] bytes
+// (row_bytes 32 or 64); boxes of box_rows whole rows of one head, swizzled over
+// the row (32 or 64 bytes), zero fill outside -- so a box never reaches into
+// the next head's rows.
+int make_map_kv4(CUtensorMap* map, const void* ptr, int64_t heads, int rows, int row_bytes, int box_rows) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(heads)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                             static_cast<cuuint64_t>(row_bytes) * static_cast<cuuint64_t>(rows)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 int64_t fp8_vt_pitch(int N) { return (static_cast<int64_t>(N) + 15) / 16 * 16; }
 
 struct Common {
@@ -586,6 +604,8 @@ int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_wo
 template <int D, int NT>
 int launch_kv4_decode(const fa::Kv4DecodeParams& p, const Kv4Plan& plan, cudaStream_t stream) {
     using C = fa::Kv4DecCfg<D, NT>;
+    CUtensorMap mv;
+    if (make_map_kv4(&mv, p.codes[1], static_cast<int64_t>(p.B) * p.Hkv, std::max(p.Nk, 8), C::ROWB, C::BN)) return FA_ERR_CUDA;
     const int items = p.B * p.Hkv * p.row_blocks;
     if (plan.cluster > 0) {
         cudaLaunchConfig_t cfg = {};
@@ -601,13 +621,13 @@ int launch_kv4_decode(const fa::Kv4DecodeParams& p, const Kv4Plan& plan, cudaStr
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         const int slot = prof_start(4, stream);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::kv4_cluster_kernel<D, NT>, p);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::kv4_cluster_kernel<D, NT>, mv, p);
         prof_stop(4, slot, stream);
         return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
     const int grid = (p.ranges + C::WARPS - 1) / C::WARPS;
     const int slot = prof_start(4, stream);
-    fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(p);
+    fa::kv4_decode_kernel<D, NT><<<grid, C::WARPS * 32, C::SMEM, stream>>>(mv, p);
     prof_stop(4, slot, stream);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     const int slot2 = prof_start(5, stream);
@@ -933,7 +953,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     fa::Kv4DecodeParams p;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.codes[0] = static_cast<const uint8_t*>(k_codes);
-    p.codes[1] = static_cast<const uint8_t*>(v_codes);
+    p.codes[1] = static_cast<const uint8_t*>(rows_k > 0 ? v_codes : q);     // a tensor map needs a base
     p.words[0] = static_cast<const uint16_t*>(k_words);
     p.words[1] = static_cast<const uint16_t*>(v_words);
     p.o = static_cast<__nv_bfloat16*>(o);

@@ -35,10 +35,10 @@
 //
 // Per tile: S^T = C^k q^T with 16 keys x 8 query rows to an mma (the codes are
 // the A operand), p from it in registers, transposed by movmatrix into the B
-// operand of O^T += C^v p^T, whose A operand pairs two keys' codes by byte
-// permutes.  Which channel sits at which mma index is free as long as q (or
-// the store of O) agrees, so each lane reads whole words of codes: for K the
-// D/4 channels of lane % 4, for V the D/8 channels of lane / 4.
+// operand of O^T += C^v p^T, whose A operand, two keys' codes in a register,
+// comes from a transposing ldmatrix over the bytes of the tile.  Which channel
+// sits at which mma index is free as long as q agrees, so of K each lane reads
+// whole words of codes, the D/4 channels of lane % 4.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -74,15 +74,17 @@ struct Kv4DecCfg {
     static constexpr int ROWB = D / 2;                    // bytes of a row's codes
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
-    // a warp's shared memory: K codes, K words, V words; V codes; (scale, zero) of K and V
-    static constexpr int OFF_V = TILE + 2 * WORDB;
-    static constexpr int OFF_SCALES = OFF_V + TILE;
-    static constexpr int WARP_BYTES = OFF_SCALES + 2 * BN * 8;
+    // a warp's shared memory: V codes (swizzled, so 512-byte aligned); K codes,
+    // K words, V words; (scale, zero) of K and V
+    static constexpr int OFF_K = TILE;
+    static constexpr int OFF_WORDS = OFF_K + TILE;
+    static constexpr int OFF_SCALES = OFF_WORDS + 2 * WORDB;
+    static constexpr int WARP_BYTES = (OFF_SCALES + 2 * BN * 8 + 511) / 512 * 512;
     static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][2]: K, V
     static constexpr int OFF_MISC = OFF_BAR + WARPS * 16;
-    static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16;
+    static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16 + 1024;
     static constexpr int OSTRIDE = D + 4;                 // floats a row of a partial output in shared memory
-    static_assert(OFF_V % 16 == 0 && TILE % 16 == 0 && WARP_BYTES % 16 == 0, "16-byte copies");
+    static_assert(TILE % 512 == 0 && OFF_WORDS % 16 == 0 && WORDB % 16 == 0, "copies and swizzle");
     static_assert(ROWS * (OSTRIDE + 2) * 4 <= WARP_BYTES, "a warp leaves its partial result in its memory");
 };
 
@@ -120,11 +122,23 @@ constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
 constexpr float kKv4Over = 256.f;      // p may grow to this before its reference moves: 2^8 times s^v below 2^7 is in fp16
 constexpr float kNoRef = 3.4028234e38f;   // minus the reference before the first score: any score then is over
 
-// Key of a 16-key tile at mma index m.  K rows 2i, 2i + 1 lie in different
-// halves of a 128-byte line (64-byte rows), as the reads of two rows at a time
-// want; and of the four keys 2t that lanes t read of V together, two lie in
-// each half.
-__host__ __device__ constexpr int kv4_key(int m) { return m ^ ((m >> 1) & 1); }
+// Keys of a 16-key tile at mma index g (and, 4 further, g + 8) of the score
+// product.  It follows from the second product, whose operand ldmatrix brings
+// in transposed: four keys of a byte column to a lane, whose codes of keys
+// (0, 2) and (1, 3) of the four pair up under the masks.  The order of the
+// rows that ldmatrix is given (kv4_v_key) is chosen so that eight of them, and
+// two K rows, fall into different banks.
+__device__ __forceinline__ int kv4_key(int g) { return (g & 3) | ((g >> 2) << 3); }
+__device__ __forceinline__ int kv4_v_key(int i) { return (i & 8) | ((i & 7) >> 1) | ((i & 1) << 2); }
+
+// Two 16 x 16 byte matrices (keys x byte columns), transposed: registers 0, 1
+// hold columns lane / 4 and lane / 4 + 8 of the first, keys 4 (lane % 4) .. + 3.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t row) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(row)
+                 : "memory");
+}
 
 struct Kv4Span {
     int nk, t0, n;      // used keys, first key tile and tiles of a sequence
@@ -194,7 +208,8 @@ struct Kv4Acc {
 // shared memory, bar_k its two barriers, `phase` their phase.  False when a
 // wait gave up.
 template <int D, int NT>
-__device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, NT>& acc, uint8_t* ring, uint64_t* bar_k,
+__device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUtensorMap* tm_v, Kv4Acc<D, NT>& acc,
+                                           uint8_t* ring, uint64_t* bar_k,
                                            uint32_t& phase, const WaitCtl& wc, int b, int hk, int r0, int nrows,
                                            int nk, int first, int count) {
     using C = Kv4DecCfg<D, NT>;
@@ -212,18 +227,22 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
             const uint32_t rows = min(C::BN, room - i * C::BN);
             const int64_t row = row0 + i * C::BN;
             mbar_arrive_expect_tx(bar_k, rows * (C::ROWB + 4));
-            bulk_load(ring, p.codes[0] + row * C::ROWB, rows * C::ROWB, bar_k);
-            bulk_load(ring + C::TILE, p.words[0] + row, rows * 2, bar_k);
-            bulk_load(ring + C::TILE + C::WORDB, p.words[1] + row, rows * 2, bar_k);
+            bulk_load(ring + C::OFF_K, p.codes[0] + row * C::ROWB, rows * C::ROWB, bar_k);
+            bulk_load(ring + C::OFF_WORDS, p.words[0] + row, rows * 2, bar_k);
+            bulk_load(ring + C::OFF_WORDS + C::WORDB, p.words[1] + row, rows * 2, bar_k);
         }
     };
     auto load_v = [&](int i) {
-        if (lane == 0) {
-            const uint32_t rows = min(C::BN, room - i * C::BN);
-            mbar_arrive_expect_tx(bar_v, rows * C::ROWB);
-            bulk_load(ring + C::OFF_V, p.codes[1] + (row0 + i * C::BN) * C::ROWB, rows * C::ROWB, bar_v);
+        if (lane == 0) {            // rows past the cache's room come as zeros
+            mbar_arrive_expect_tx(bar_v, C::TILE);
+            tma_load_3d(ring, tm_v, bar_v, 0, (first + i) * C::BN, b * p.Hkv + hk);
         }
     };
+    // this lane's row and 16-byte chunk for ldmatrix, and the next two chunks'
+    const int v_key = kv4_v_key(lane & 15);
+    const uint32_t v_row = smem_u32(ring) + v_key * C::ROWB;
+    const uint32_t v_at = v_row + (D == 128 ? ((lane >> 4) ^ ((v_key >> 1) & 3)) : ((lane >> 4) ^ ((v_key >> 2) & 1))) * 16;
+    const int kkey = kv4_key(g8);
     if (count > 0) {
         load_k(0);
         load_v(0);
@@ -303,13 +322,13 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
 
     for (int i = 0; i < count; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_k, phase, wc))) return false;
-        const uint8_t* st = ring;
+        const uint8_t* st = ring + C::OFF_K;
         const int k0 = (first + i) * C::BN;
 
         // ---- scales and zeros: a key a lane
         const bool edge = k0 + C::BN > nk;
         {
-            const uint16_t* ws = reinterpret_cast<const uint16_t*>(st + C::TILE);
+            const uint16_t* ws = reinterpret_cast<const uint16_t*>(ring + C::OFF_WORDS);
             uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
 #pragma unroll
             for (int kk = 0; kk < C::BN / 32; ++kk) {
@@ -368,8 +387,8 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
 #pragma unroll
         for (int m = 0; m < C::MT; ++m) {
             uint32_t ka[W], kb[W];
-            const uint8_t* ra = st + (m * 16 + kv4_key(g8)) * C::ROWB + t4 * (W * 4);
-            const uint8_t* rb = ra + 8 * C::ROWB;
+            const uint8_t* ra = st + (m * 16 + kkey) * C::ROWB + t4 * (W * 4);
+            const uint8_t* rb = ra + 4 * C::ROWB;
             if constexpr (D == 128) {
                 const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
                 ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
@@ -399,7 +418,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
         for (int m = 0; m < C::MT; ++m)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float2 sz = sck[m * 16 + half * 8 + kv4_key(g8)];
+                const float2 sz = sck[m * 16 + half * 4 + kkey];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
@@ -410,7 +429,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
             for (int m = 0; m < C::MT; ++m)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int key = k0 + m * 16 + half * 8 + kv4_key(g8);
+                    const int key = k0 + m * 16 + half * 4 + kkey;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
@@ -476,7 +495,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
         for (int m = 0; m < C::MT; ++m)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float2 sz = scv[m * 16 + half * 8 + kv4_key(g8)];
+                const float2 sz = scv[m * 16 + half * 4 + kkey];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float2 w = fmul2(e[m][nt][half], make_float2(sz.x, sz.x));
@@ -486,39 +505,21 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
             }
         // ---- O^T += C^v (p s^v)^T
         if (!__all_sync(0xffffffffu, mbar_wait(bar_v, phase, wc))) return false;
-        const uint8_t* sv = ring + C::OFF_V;
 #pragma unroll
-        for (int m = 0; m < C::MT; ++m) {
-            constexpr int VW = D / 64;                 // words of codes a lane and key
-            uint32_t v[4][VW];                         // mma indices 2t, 2t+1, 2t+8, 2t+9
+        for (int m = 0; m < C::MT; ++m)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int row = m * 16 + (kk >> 1) * 8 + kv4_key(2 * t4 + (kk & 1));
-                const uint8_t* src = sv + row * C::ROWB + g8 * (VW * 4);
-                if constexpr (D == 128) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(src);
-                    v[kk][0] = u.x;
-                    v[kk][VW - 1] = u.y;
-                } else {
-                    v[kk][0] = *reinterpret_cast<const uint32_t*>(src);
+            for (int c2 = 0; c2 < D / 64; ++c2) {          // two chunks of 16 bytes
+                uint32_t v[4];
+                load_transposed(v, (c2 ? v_at ^ 32u : v_at) + m * 16 * C::ROWB);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t u = v[k], u8 = u >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(oacc[c2 * 4 + k][nt], u & kNibLo, u & kNibHi, u8 & kNibLo, u8 & kNibHi, pf[m][nt][0],
+                                pf[m][nt][1]);
                 }
             }
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-#pragma unroll
-                for (int up = 0; up < 2; ++up) {       // codes 0-3, then 4-7 of the word
-                    const uint32_t sel = up ? 0x7632u : 0x5410u;
-                    const uint32_t u = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-                    const uint32_t u8 = u >> 8, y8 = y >> 8;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(oacc[w * 4 + up * 2][nt], u & kNibLo, u & kNibHi, y & kNibLo, y & kNibHi,
-                                pf[m][nt][0], pf[m][nt][1]);
-                        mma_f16(oacc[w * 4 + up * 2 + 1][nt], u8 & kNibLo, u8 & kNibHi, y8 & kNibLo, y8 & kNibHi,
-                                pf[m][nt][0], pf[m][nt][1]);
-                    }
-                }
-        }
         __syncwarp();               // and V
         if (i + 1 < count) load_v(i + 1);
         phase ^= 1;
@@ -527,8 +528,8 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, Kv4Acc<D, N
     return true;
 }
 
-// Hands each of the warp's query rows to put(row, channels from g8 * D/8 on,
-// reference, sum): a lane of each g8 has D/8 channels of two rows of each nt.
+// Hands each of the warp's query rows to put(row, values, reference, sum): a
+// lane has channels 16 m + 2 g8 + {0, 1}, m < D / 16, of two rows of each nt.
 // O is left as it is (relative to the reference).
 template <int D, int NT, typename Put>
 __device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, int nrows, const Put& put) {
@@ -599,9 +600,10 @@ __device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4DecCfg<D, NT>::WARPS * 32, Kv4DecCfg<D, NT>::MIN_CTAS)
-kv4_cluster_kernel(const Kv4DecodeParams p) {
+kv4_cluster_kernel(const __grid_constant__ CUtensorMap tm_v, const Kv4DecodeParams p) {
     using C = Kv4DecCfg<D, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_smem_1024(smem_raw);
     const int warp = threadIdx.x >> 5, lane = lane_id(), g8 = lane >> 2;
     const int ctas = cluster_size(), rank = cluster_rank();
     uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * 2;
@@ -624,16 +626,16 @@ kv4_cluster_kernel(const Kv4DecodeParams p) {
     const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
     uint32_t phase = 0;
     Kv4Acc<D, NT> acc;
-    const bool ok = kv4_attend<D, NT>(p, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
+    const bool ok = kv4_attend<D, NT>(p, &tm_v, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
                                       sp.t0 + t0, t1 - t0);
     if (!ok) kv4_drain(bar_k, phase, p.error_word);
     auto partial = [&](int w) { return reinterpret_cast<float*>(smem + w * C::WARP_BYTES); };   // [ROWS][OSTRIDE]
     auto stats = [&](int w) { return partial(w) + C::ROWS * C::OSTRIDE; };                      // [ROWS][2]
-    kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float m, float l) {
-        float4* dst = reinterpret_cast<float4*>(partial(warp) + r * C::OSTRIDE + g8 * (D / 8));
+    kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
+        float2* dst = reinterpret_cast<float2*>(partial(warp) + r * C::OSTRIDE + 2 * g8);
 #pragma unroll
-        for (int v = 0; v < D / 32; ++v) dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
-        if (g8 == 0) *reinterpret_cast<float2*>(stats(warp) + 2 * r) = make_float2(m, l);
+        for (int m = 0; m < D / 16; ++m) dst[8 * m] = make_float2(a[2 * m], a[2 * m + 1]);
+        if (g8 == 0) *reinterpret_cast<float2*>(stats(warp) + 2 * r) = make_float2(ref, l);
     });
     __syncthreads();
     constexpr int V = D / 32;
@@ -690,11 +692,12 @@ struct Kv4Cut {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv4DecCfg<D, NT>::WARPS * 32, Kv4DecCfg<D, NT>::MIN_CTAS)
-kv4_decode_kernel(const Kv4DecodeParams p) {
+kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_v, const Kv4DecodeParams p) {
     using C = Kv4DecCfg<D, NT>;
     // the merge launched after this grid may be scheduled now
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_smem_1024(smem_raw);
     const int warp = threadIdx.x >> 5, lane = lane_id(), g8 = lane >> 2;
     const int per = p.Hkv * p.row_blocks;
     uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * 2;
@@ -770,30 +773,28 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         const int hk = item / p.row_blocks;
         const int r0 = (item - hk * p.row_blocks) * C::ROWS, nrows = min(C::ROWS, p.Nq * p.G - r0);
         Kv4Acc<D, NT> acc;
-        if (!kv4_attend<D, NT>(p, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
+        if (!kv4_attend<D, NT>(p, &tm_v, acc, smem + warp * C::WARP_BYTES, bar_k, phase, wc, b, hk, r0, nrows, sp.nk,
                                sp.t0 + tile0, count)) {
             kv4_drain(bar_k, phase, p.error_word);
             return;
         }
         const bool whole = count == sp.n;
-        kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float m, float l) {
+        kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
             if (whole) {
                 const bool some = !(l == 0.f);      // a NaN sum stays NaN
                 const float inv = some ? 1.f / l : 0.f;
                 size_t lse_at;
                 const size_t row = kv4_out_row(p, b, hk, r0 + r, lse_at);
-                uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + g8 * (D / 8));
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + 2 * g8);
 #pragma unroll
-                for (int v = 0; v < D / 64; ++v)
-                    dst[v] = make_uint4(pack_bf16(a[8 * v] * inv, a[8 * v + 1] * inv), pack_bf16(a[8 * v + 2] * inv, a[8 * v + 3] * inv),
-                                        pack_bf16(a[8 * v + 4] * inv, a[8 * v + 5] * inv), pack_bf16(a[8 * v + 6] * inv, a[8 * v + 7] * inv));
-                if (g8 == 0) p.lse[lse_at] = some ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+                for (int m = 0; m < D / 16; ++m) dst[8 * m] = pack_bf16(a[2 * m] * inv, a[2 * m + 1] * inv);
+                if (g8 == 0) p.lse[lse_at] = some ? (ref + __log2f(l)) * 0.6931471805599453f : -INFINITY;
             } else {
                 const size_t at_row = (static_cast<size_t>(range) * 2 + (tile0 == 0)) * C::ROWS + r;
-                float4* dst = reinterpret_cast<float4*>(p.o_part + at_row * D + g8 * (D / 8));
+                float2* dst = reinterpret_cast<float2*>(p.o_part + at_row * D + 2 * g8);
 #pragma unroll
-                for (int v = 0; v < D / 32; ++v) dst[v] = make_float4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
-                if (g8 == 0) p.ml_part[at_row] = make_float2(m, l);
+                for (int m = 0; m < D / 16; ++m) dst[8 * m] = make_float2(a[2 * m], a[2 * m + 1]);
+                if (g8 == 0) p.ml_part[at_row] = make_float2(ref, l);
             }
         });
         x += count;
