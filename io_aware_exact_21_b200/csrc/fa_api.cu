@@ -232,21 +232,18 @@ int make_map_u8_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-// Tensor map over the V codes of a 4-bit cache, [heads, rows, row_bytes] bytes
-// (row_bytes 32 or 64); boxes of box_rows whole rows of one head, swizzled over
-// the row (32 or 64 bytes), zero fill outside -- so a box never reaches into
-// the next head's rows.
-int make_map_kv4(CUtensorMap* map, const void* ptr, int64_t heads, int rows, int row_bytes, int box_rows) {
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(heads)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
-                             static_cast<cuuint64_t>(row_bytes) * static_cast<cuuint64_t>(rows)};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_rows), 1};
+// Tensor map over the V codes of a 4-bit cache as lines of 128 bytes (2 or 4
+// rows), [heads, lines, 128]; boxes of box_lines lines of one head, 128-byte
+// swizzle, zero fill outside -- so a box never reaches into the next head.
+int make_map_kv4(CUtensorMap* map, const void* ptr, int64_t heads, int64_t lines, int box_lines) {
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(lines), static_cast<cuuint64_t>(heads)};
+    cuuint64_t strides[2] = {128, 128 * static_cast<cuuint64_t>(lines)};
+    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_lines), 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -605,7 +602,8 @@ template <int D, int NT>
 int launch_kv4_decode(const fa::Kv4DecodeParams& p, const Kv4Plan& plan, cudaStream_t stream) {
     using C = fa::Kv4DecCfg<D, NT>;
     CUtensorMap mv;
-    if (make_map_kv4(&mv, p.codes[1], static_cast<int64_t>(p.B) * p.Hkv, std::max(p.Nk, 8), C::ROWB, C::BN)) return FA_ERR_CUDA;
+    if (make_map_kv4(&mv, p.codes[1], static_cast<int64_t>(p.B) * p.Hkv,
+                     std::max(p.Nk, 8) * static_cast<int64_t>(C::ROWB) / 128, C::TILE / 128)) return FA_ERR_CUDA;
     const int items = p.B * p.Hkv * p.row_blocks;
     if (plan.cluster > 0) {
         cudaLaunchConfig_t cfg = {};

@@ -74,17 +74,17 @@ struct Kv4DecCfg {
     static constexpr int ROWB = D / 2;                    // bytes of a row's codes
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
-    // a warp's shared memory: V codes (swizzled, so 512-byte aligned); K codes,
+    // a warp's shared memory: V codes (swizzled, so 1024-byte aligned); K codes,
     // K words, V words; (scale, zero) of K and V
     static constexpr int OFF_K = TILE;
     static constexpr int OFF_WORDS = OFF_K + TILE;
     static constexpr int OFF_SCALES = OFF_WORDS + 2 * WORDB;
-    static constexpr int WARP_BYTES = (OFF_SCALES + 2 * BN * 8 + 511) / 512 * 512;
+    static constexpr int WARP_BYTES = (OFF_SCALES + 2 * BN * 8 + 1023) / 1024 * 1024;
     static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][2]: K, V
     static constexpr int OFF_MISC = OFF_BAR + WARPS * 16;
     static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16 + 1024;
     static constexpr int OSTRIDE = D + 4;                 // floats a row of a partial output in shared memory
-    static_assert(TILE % 512 == 0 && OFF_WORDS % 16 == 0 && WORDB % 16 == 0, "copies and swizzle");
+    static_assert(TILE % 1024 == 0 && OFF_WORDS % 16 == 0 && WORDB % 16 == 0, "copies and swizzle");
     static_assert(ROWS * (OSTRIDE + 2) * 4 <= WARP_BYTES, "a warp leaves its partial result in its memory");
 };
 
@@ -235,13 +235,16 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
     auto load_v = [&](int i) {
         if (lane == 0) {            // rows past the cache's room come as zeros
             mbar_arrive_expect_tx(bar_v, C::TILE);
-            tma_load_3d(ring, tm_v, bar_v, 0, (first + i) * C::BN, b * p.Hkv + hk);
+            tma_load_3d(ring, tm_v, bar_v, 0, (first + i) * (C::TILE / 128), b * p.Hkv + hk);
         }
     };
-    // this lane's row and 16-byte chunk for ldmatrix, and the next two chunks'
+    // this lane's row for ldmatrix (its first 16-byte chunk; two chunks on the
+    // address differs in bit 5): the tile lies in 128-byte lines of 2 or 4 keys,
+    // whose chunks are exchanged by the line's index
+    constexpr int KPL = 128 / C::ROWB;                       // keys a line
     const int v_key = kv4_v_key(lane & 15);
-    const uint32_t v_row = smem_u32(ring) + v_key * C::ROWB;
-    const uint32_t v_at = v_row + (D == 128 ? ((lane >> 4) ^ ((v_key >> 1) & 3)) : ((lane >> 4) ^ ((v_key >> 2) & 1))) * 16;
+    const uint32_t v_at = smem_u32(ring) + v_key / KPL * 128 +
+                          ((((v_key % KPL) * (8 / KPL)) | (lane >> 4)) ^ (v_key / KPL)) * 16;
     const int kkey = kv4_key(g8);
     if (count > 0) {
         load_k(0);
@@ -510,7 +513,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
 #pragma unroll
             for (int c2 = 0; c2 < D / 64; ++c2) {          // two chunks of 16 bytes
                 uint32_t v[4];
-                load_transposed(v, (c2 ? v_at ^ 32u : v_at) + m * 16 * C::ROWB);
+                load_transposed(v, (v_at ^ ((c2 ? 32u : 0u) | (D == 64 && (m & 1) ? 64u : 0u))) + m * 16 * C::ROWB);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t u = v[k], u8 = u >> 8;
