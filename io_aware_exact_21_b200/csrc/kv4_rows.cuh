@@ -83,53 +83,71 @@ __device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t bf2_min_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Codes of 8 channels (one bf16 pair a word) of a row, and the row's word.
 // LANES neighbouring lanes hold the row.
 //
-// s: hi - lo rounded up to fp32 and divided by 15 rounding up, then rounded up
-// to 4 significant bits.  15 s and s are fp32 numbers, so comparing them with
-// a value rounded up decides as the exact value does.  (Halved first, so that
-// the sum cannot overflow.)
+// s: with r = hi - lo rounded up to fp32 (halved, so that it cannot overflow),
+// r (1 - 2^-21) / 15 rounded up to 4 significant bits is s or the number below
+// it, which 15 s >= r tells apart: 15 s is an fp32 number, so it compares with
+// r as with the exact difference.
 //
 // c: x / s is either exactly half-way between two integers or at least 2^-10
 // away from that (8 bits over 4 bits), while x * (1 / s) + z errs by less than
-// 2^-18; so adding 1/2 + 2^-11 before cutting the fraction gives the nearest
+// 2^-17; so adding 1/2 + 2^-11 before cutting the fraction gives the nearest
 // integer with exact ties upwards.  Adding 128 as well puts the integer into
 // the third byte of the fp32 pattern, from where byte permutes collect it.
+// c = 16 needs hi / s and -lo / s both half-way and 15 together.
+//
+// The instructions bound this, not the memory, when they are many: with the
+// division and the reciprocal of the library's rounding, and a minimum a value,
+// 1.39 GB took 221 us at the start and 155 us with this.
 template <int LANES>
 __device__ __forceinline__ uint32_t kv4_encode(const uint4& x, uint32_t& word) {
-    constexpr uint32_t kSign = 0x80008000u;
-    uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
-    uint32_t dn = bf2_max_nan(bf2_max_nan(x.x ^ kSign, x.y ^ kSign), bf2_max_nan(x.z ^ kSign, x.w ^ kSign));
-    // low half: the larger value of `up`'s halves, high half: of `dn`'s
+    const uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
+    const uint32_t dn = bf2_min_nan(bf2_min_nan(x.x, x.y), bf2_min_nan(x.z, x.w)) ^ 0x80008000u;
+    // low half: the larger of `up`'s halves, high half: of `dn`'s
     uint32_t m = bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) m = bf2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = bf2_max_nan(m, 0u);
     const float hi = __uint_as_float(m << 16), neg_lo = __uint_as_float(m & 0xffff0000u);
-    const float y = __fdiv_ru(__fadd_ru(0.5f * hi, 0.5f * neg_lo), 7.5f);
-    const uint32_t sb = max((__float_as_uint(y) + 0x000fffffu) & 0xfff00000u, 0x00800000u);
+    const float r = __fmaf_ru(hi, 0.5f, 0.5f * neg_lo);
+    uint32_t sb = (__float_as_uint(r * (0.13333333f * (1.f - 1.f / 2097152.f))) + 0x000fffffu) & 0xfff00000u;
+    sb = max(sb + (7.5f * __uint_as_float(sb) < r ? 0x00100000u : 0u), 0x00800000u);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(sb)));
+    constexpr float kHalfUp = 0.5f + 1.f / 2048.f;
+    const uint32_t zb = __float_as_uint(fmaf(neg_lo, inv, 128.f + kHalfUp));
+    const float base = __uint_as_float(zb & 0xffff0000u) + kHalfUp;         // 128 + z + 1/2 and a little
+    word = (sb | (zb & 0x000f0000u)) >> 16;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    float e[4], o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        e[j] = fmaf(__uint_as_float(xs[j] << 16), inv, base);
+        o[j] = fmaf(__uint_as_float(xs[j] & 0xffff0000u), inv, base);
+    }
+    if (fmaf(hi, inv, base) >= 144.f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            e[j] = fminf(e[j], 143.9f);
+            o[j] = fminf(o[j], 143.9f);
+        }
+    }
+    auto third = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0062); };
+    const uint32_t even = __byte_perm(third(e[0], e[1]), third(e[2], e[3]), 0x5410);
+    const uint32_t odd = __byte_perm(third(o[0], o[1]), third(o[2], o[3]), 0x5410);
     if (!(hi <= 3.4e38f && neg_lo <= 3.4e38f)) {
         word = kKv4NaN;
         return 0u;
     }
-    const float inv = __frcp_rn(__uint_as_float(sb));
-    constexpr float kHalfUp = 0.5f + 1.f / 2048.f;
-    const float z = floorf(fmaf(neg_lo, inv, kHalfUp));
-    word = (sb >> 16) | static_cast<uint32_t>(z);
-    const float base = 128.f + kHalfUp + z;
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    uint32_t e[4], o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float a = fmaf(__uint_as_float(xs[j] << 16), inv, base);
-        const float b = fmaf(__uint_as_float(xs[j] & 0xffff0000u), inv, base);
-        e[j] = __float_as_uint(fminf(a, 143.9f));
-        o[j] = __float_as_uint(fminf(b, 143.9f));
-    }
-    const uint32_t even = __byte_perm(__byte_perm(e[0], e[1], 0x0062), __byte_perm(e[2], e[3], 0x0062), 0x5410);
-    const uint32_t odd = __byte_perm(__byte_perm(o[0], o[1], 0x0062), __byte_perm(o[2], o[3], 0x0062), 0x5410);
-    return even | (odd << 4);
+    return even + odd * 16u;
 }
 
 // The 8 channels of a word of codes as bf16.  128 + c - (128 + z) and the
@@ -165,20 +183,13 @@ constexpr int kKv4Warps = 8;
 template <int D, int ITER>
 __host__ __device__ constexpr int kv4_tokens() { return ITER * (32 / (D / 8)); }
 
-// Sequence and cache row of each of a warp's tokens: lane j holds token j's
-// (pos < 0: not taken).
+// Rows of the cache arrays of a warp's tokens and head h: lane j holds token
+// j's (below 0: not taken).
 template <int TOK>
-__device__ __forceinline__ void kv4_warp_places(const Kv4Params& p, int64_t first, int& b, int& pos) {
-    const int lane = lane_id();
-    b = 0;
-    pos = -1;
-    if (lane < TOK) {
-        int bb, pp;
-        if (kv4_place(p.place, first + lane, p.rows, bb, pp)) {
-            b = bb;
-            pos = pp;
-        }
-    }
+__device__ __forceinline__ int64_t kv4_warp_rows(const Kv4Params& p, int64_t first, int h) {
+    int b, pos;
+    if (lane_id() >= TOK || !kv4_place(p.place, first + lane_id(), p.rows, b, pos)) return -1;
+    return (static_cast<int64_t>(b) * p.place.H + h) * p.place.Nk + pos;
 }
 
 // Writes bf16 rows into the cache.  blockIdx.y selects K or V.
@@ -204,20 +215,18 @@ kv4_write_kernel(const Kv4Params p) {
         v[it] = r < p.rows ? __ldcs(reinterpret_cast<const uint4*>(x + (r * H + h) * D + c8 * 8))
                            : make_uint4(0, 0, 0, 0);
     }
-    int tb, tpos;
-    kv4_warp_places<TOK>(p, first, tb, tpos);
+    const int64_t row = kv4_warp_rows<TOK>(p, first, h);
+    uint32_t mine = 0;              // the word of token `lane`
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
         uint32_t word;
         const uint32_t c = kv4_encode<LANES>(v[it], word);
-        const int b = __shfl_sync(0xffffffffu, tb, it * ROWS + sub);
-        const int pos = __shfl_sync(0xffffffffu, tpos, it * ROWS + sub);
-        if (pos >= 0) {
-            const int64_t row = (static_cast<int64_t>(b) * H + h) * p.place.Nk + pos;
-            *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + c8 * 4) = c;
-            if (c8 == 0) words[row] = static_cast<uint16_t>(word);
-        }
+        const int64_t to = __shfl_sync(0xffffffffu, row, it * ROWS + sub);
+        if (to >= 0) *reinterpret_cast<uint32_t*>(codes + to * (D / 2) + c8 * 4) = c;
+        word = __shfl_sync(0xffffffffu, word, lane % ROWS * LANES);
+        if (lane / ROWS == it) mine = word;
     }
+    if (row >= 0) words[row] = static_cast<uint16_t>(mine);
 }
 
 // Reads cache rows back as bf16.  poison (attention's own use): a token whose
@@ -239,18 +248,15 @@ kv4_read_kernel(const Kv4Params p) {
     const uint16_t* other = blockIdx.y ? p.words[0] : p.words[1];
     __nv_bfloat16* x = blockIdx.y ? p.x[1] : p.x[0];
     const int sub = lane / LANES, c8 = lane % LANES;
-    int tb, tpos;
-    kv4_warp_places<TOK>(p, first, tb, tpos);
+    const int64_t from = kv4_warp_rows<TOK>(p, first, h);
     uint32_t c[ITER], word[ITER];
     bool taken[ITER];
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-        const int b = __shfl_sync(0xffffffffu, tb, it * ROWS + sub);
-        const int pos = __shfl_sync(0xffffffffu, tpos, it * ROWS + sub);
-        taken[it] = pos >= 0;
+        const int64_t row = __shfl_sync(0xffffffffu, from, it * ROWS + sub);
+        taken[it] = row >= 0;
         c[it] = word[it] = 0;
         if (taken[it]) {
-            const int64_t row = (static_cast<int64_t>(b) * H + h) * p.place.Nk + pos;
             c[it] = *reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + c8 * 4);
             word[it] = words[row];
             if (p.poison) {
