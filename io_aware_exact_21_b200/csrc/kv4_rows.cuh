@@ -89,9 +89,25 @@ __device__ __forceinline__ uint32_t bf2_min_nan(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Codes of 8 channels (one bf16 pair a word) of a row, and the row's word.
-// LANES neighbouring lanes hold the row.
-//
+// {low: max x, high: -min x} of a row that LANES neighbouring lanes hold, 8
+// channels (one bf16 pair a word) each; NaN where x has one.
+template <int LANES>
+__device__ __forceinline__ uint32_t kv4_reduce(const uint4& x) {
+    const uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
+    const uint32_t dn = bf2_min_nan(bf2_min_nan(x.x, x.y), bf2_min_nan(x.z, x.w)) ^ 0x80008000u;
+    uint32_t m = bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = bf2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// How a row is rounded: x * inv + base cut to an integer is 128 + c.
+struct Kv4Scale {
+    float inv, base;
+    uint32_t word;
+    bool clamp;         // c = 16 can come out
+};
+
 // s: with r = hi - lo rounded up to fp32 (halved, so that it cannot overflow),
 // r (1 - 2^-21) / 15 rounded up to 4 significant bits is s or the number below
 // it, which 15 s >= r tells apart: 15 s is an fp32 number, so it compares with
@@ -100,32 +116,27 @@ __device__ __forceinline__ uint32_t bf2_min_nan(uint32_t a, uint32_t b) {
 // c: x / s is either exactly half-way between two integers or at least 2^-10
 // away from that (8 bits over 4 bits), while x * (1 / s) + z errs by less than
 // 2^-17; so adding 1/2 + 2^-11 before cutting the fraction gives the nearest
-// integer with exact ties upwards.  Adding 128 as well puts the integer into
-// the third byte of the fp32 pattern, from where byte permutes collect it.
-// c = 16 needs hi / s and -lo / s both half-way and 15 together.
-//
-// The instructions bound this, not the memory, when they are many: with the
-// division and the reciprocal of the library's rounding, and a minimum a value,
-// 1.39 GB took 221 us at the start and 155 us with this.
-template <int LANES>
-__device__ __forceinline__ uint32_t kv4_encode(const uint4& x, uint32_t& word) {
-    const uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
-    const uint32_t dn = bf2_min_nan(bf2_min_nan(x.x, x.y), bf2_min_nan(x.z, x.w)) ^ 0x80008000u;
-    // low half: the larger of `up`'s halves, high half: of `dn`'s
-    uint32_t m = bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = bf2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+// integer with exact ties upwards.  c = 16 needs hi / s and -lo / s both
+// half-way and 15 together.
+__device__ __forceinline__ Kv4Scale kv4_scale(uint32_t m) {
     m = bf2_max_nan(m, 0u);
     const float hi = __uint_as_float(m << 16), neg_lo = __uint_as_float(m & 0xffff0000u);
     const float r = __fmaf_ru(hi, 0.5f, 0.5f * neg_lo);
     uint32_t sb = (__float_as_uint(r * (0.13333333f * (1.f - 1.f / 2097152.f))) + 0x000fffffu) & 0xfff00000u;
     sb = max(sb + (7.5f * __uint_as_float(sb) < r ? 0x00100000u : 0u), 0x00800000u);
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(sb)));
+    Kv4Scale s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(__uint_as_float(sb)));
     constexpr float kHalfUp = 0.5f + 1.f / 2048.f;
-    const uint32_t zb = __float_as_uint(fmaf(neg_lo, inv, 128.f + kHalfUp));
-    const float base = __uint_as_float(zb & 0xffff0000u) + kHalfUp;         // 128 + z + 1/2 and a little
-    word = (sb | (zb & 0x000f0000u)) >> 16;
+    const uint32_t zb = __float_as_uint(fmaf(neg_lo, s.inv, 128.f + kHalfUp));
+    s.base = __uint_as_float(zb & 0xffff0000u) + kHalfUp;           // 128 + z + 1/2 and a little
+    s.word = hi <= 3.4e38f && neg_lo <= 3.4e38f ? (sb | (zb & 0x000f0000u)) >> 16 : kKv4NaN;
+    s.clamp = fmaf(hi, s.inv, s.base) >= 144.f;
+    return s;
+}
+
+// Codes of 8 channels.  128 + c has c in the third byte of its fp32 pattern,
+// from where byte permutes collect it.
+__device__ __forceinline__ uint32_t kv4_encode(const uint4& x, float inv, float base, bool clamp) {
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
     float e[4], o[4];
 #pragma unroll
@@ -133,7 +144,7 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint4& x, uint32_t& word) {
         e[j] = fmaf(__uint_as_float(xs[j] << 16), inv, base);
         o[j] = fmaf(__uint_as_float(xs[j] & 0xffff0000u), inv, base);
     }
-    if (fmaf(hi, inv, base) >= 144.f) {
+    if (clamp) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             e[j] = fminf(e[j], 143.9f);
@@ -143,10 +154,6 @@ __device__ __forceinline__ uint32_t kv4_encode(const uint4& x, uint32_t& word) {
     auto third = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0062); };
     const uint32_t even = __byte_perm(third(e[0], e[1]), third(e[2], e[3]), 0x5410);
     const uint32_t odd = __byte_perm(third(o[0], o[1]), third(o[2], o[3]), 0x5410);
-    if (!(hi <= 3.4e38f && neg_lo <= 3.4e38f)) {
-        word = kKv4NaN;
-        return 0u;
-    }
     return even + odd * 16u;
 }
 
@@ -193,6 +200,13 @@ __device__ __forceinline__ int64_t kv4_warp_rows(const Kv4Params& p, int64_t fir
 }
 
 // Writes bf16 rows into the cache.  blockIdx.y selects K or V.
+//
+// Instructions bound it as soon as there are many a value (the integer pipe
+// does half of them): a row's scale is found by one lane, lane j for token j,
+// once its maxima are there, not by all that hold the row.  At 1.39 GB read
+// and written: 221 us with the library's correctly rounded division and
+// reciprocal by every lane, 155 us with approximations that are exact here,
+// 126 us with a lane to a token.
 template <int D, int ITER>
 __global__ void __launch_bounds__(kKv4Warps * 32)
 kv4_write_kernel(const Kv4Params p) {
@@ -216,17 +230,23 @@ kv4_write_kernel(const Kv4Params p) {
                            : make_uint4(0, 0, 0, 0);
     }
     const int64_t row = kv4_warp_rows<TOK>(p, first, h);
-    uint32_t mine = 0;              // the word of token `lane`
+    uint32_t mine = 0;              // the maxima of token `lane`
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-        uint32_t word;
-        const uint32_t c = kv4_encode<LANES>(v[it], word);
-        const int64_t to = __shfl_sync(0xffffffffu, row, it * ROWS + sub);
-        if (to >= 0) *reinterpret_cast<uint32_t*>(codes + to * (D / 2) + c8 * 4) = c;
-        word = __shfl_sync(0xffffffffu, word, lane % ROWS * LANES);
-        if (lane / ROWS == it) mine = word;
+        const uint32_t m = __shfl_sync(0xffffffffu, kv4_reduce<LANES>(v[it]), lane % ROWS * LANES);
+        if (lane / ROWS == it) mine = m;
     }
-    if (row >= 0) words[row] = static_cast<uint16_t>(mine);
+    const Kv4Scale s = kv4_scale(mine);
+    const bool clamp = __any_sync(0xffffffffu, s.clamp);
+    if (row >= 0) words[row] = static_cast<uint16_t>(s.word);
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+        const float inv = __shfl_sync(0xffffffffu, s.inv, it * ROWS + sub);
+        const float base = __shfl_sync(0xffffffffu, s.base, it * ROWS + sub);
+        const int64_t to = __shfl_sync(0xffffffffu, row, it * ROWS + sub);
+        const uint32_t c = kv4_encode(v[it], inv, base, clamp);
+        if (to >= 0) *reinterpret_cast<uint32_t*>(codes + to * (D / 2) + c8 * 4) = c;
+    }
 }
 
 // Reads cache rows back as bf16.  poison (attention's own use): a token whose
