@@ -227,9 +227,10 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * used.  Queries without a key get O = 0, LSE = -inf.  A row whose K or V
  * stands for NaN makes O NaN (and LSE unspecified) for the queries that see
  * it, and reaches no others.
- *   Up to 32 query rows to a key/value head (Nq * H / Hkv) run on a kernel
- * that multiplies the 4-bit codes as they are; more are run by reading the
- * rows in use back into the workspace for the tensor-core forward.
+ *   Few query rows to a key/value head (Nq * H / Hkv; up to 96 with a head
+ * each, 192 with four to a head) run on kernels that multiply the 4-bit codes
+ * as they are; more are run by reading the rows in use back into the workspace
+ * for the tensor-core forward.
  *   num_splits : few rows: the keys of all sequences and heads together are
  * cut into equal ranges, num_splits to each (sequence, key/value head) on
  * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.

@@ -458,15 +458,17 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
 }
 
 // ------------------------------------------------------ 4-bit K/V cache --
-#ifndef KV4_CLUSTER_TILES
-#define KV4_CLUSTER_TILES 4
-#endif
-constexpr int kKv4DirectRows = 32;
-
-// Whether attention over the 4-bit cache runs on kv4_decode_kernel (query rows
-// to a key/value head: Nq * group) or reads the cache back for the forward.
+// Whether attention over the 4-bit cache multiplies the codes as they are, 16
+// query rows to a warp, or reads the rows back for the forward, whose blocks
+// hold 256 queries of one head.  The one's time goes with the rows, Nq * group;
+// the other's with the blocks of the group's heads, whatever they hold, and
+// with the rows read back.  Measured (us, codes / read back), B 16, 8 kv heads,
+// 8192 rows, d 128: group 1 and 64 queries 120 / 257; group 4 and 32 queries
+// 226 / 525, 64 queries 429 / 527; B 32, 2 kv heads, 1000 rows, d 64, group 4:
+// 16 queries 14 / 44, 64 queries 54 / 44.
 bool kv4_direct(int Nq, int group, int Nk) {
-    return static_cast<int64_t>(Nq) * group <= kKv4DirectRows || Nk == 0;
+    const int64_t blocks = static_cast<int64_t>(group) * ((Nq + 255) / 256);
+    return static_cast<int64_t>(Nq) * group <= 64 + 32 * blocks || Nk == 0;
 }
 
 // Query rows a CTA of kv4_decode_kernel holds: 8 or 16.
@@ -477,8 +479,15 @@ int64_t kv4_row_blocks(int64_t rows) {
     return (rows + per - 1) / per;
 }
 
-// How the key tiles are dealt out: to a cluster of `cluster` CTAs each item, or
-// (cluster 0) in `ranges` equal ranges, with a merge after it.
+// How the key tiles are dealt out: to a cluster of `cluster` CTAs each item
+// (kv4_cluster_kernel), or (cluster 0) in `ranges` equal ranges with a merge
+// after it (kv4_decode_kernel).  The first is one launch without a workspace,
+// but leaves warps idle where sequences differ, and SMs where items are few; it
+// is taken while all its CTAs run at once and a warp has 6 tiles at most.
+// Measured (us on the device, cluster / ranges), d 128, one query row to each
+// of 8 kv heads: B 4, 1024 rows 7.1 / 9.9, 8192 rows (4 tiles) 13.1 / 15.9,
+// 16384 rows (8 tiles) 19.7 / 20.7, there with lengths from 0 up 17.8 / 16.8;
+// B 40, 1024 rows (4 tiles) 14.2 / 16.9, 4096 rows (16 tiles) 42.5 / 37.5.
 struct Kv4Plan {
     int cluster, ranges;
 };
@@ -494,7 +503,7 @@ Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_
     const int64_t tiles = (keys + C1::BN - 1) / C1::BN;
     int cluster = 8;
     while (cluster > 1 && (items * cluster > ctas || tiles <= C1::WARPS * cluster / 2)) cluster /= 2;
-    if (items * cluster <= ctas && tiles <= KV4_CLUSTER_TILES * C1::WARPS * cluster) return {cluster, 0};
+    if (items * cluster <= ctas && tiles <= 6 * C1::WARPS * cluster) return {cluster, 0};
     return {0, ctas * C1::WARPS};
 }
 
