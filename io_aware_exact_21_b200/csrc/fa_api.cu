@@ -432,11 +432,11 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
     p.error_word = st->error_word;
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
     p.fault_skip_v = 0;
-    p.nsplit = ns;
+    p.nsplit = static_cast<short>(ns);
     p.kv.seqused_k = seqlens_k;
     p.kv.o_part = ns > 1 ? part : nullptr;
     p.kv.lse_part = ns > 1 ? part + static_cast<size_t>(ns) * rows_q * H * d : nullptr;
-    p.kv.group = group;
+    p.group = static_cast<unsigned short>(group);
     int grid = st->num_sms;
     const int64_t items = static_cast<int64_t>(B) * H * ns * ((Nq + 255) / 256);
     if (items < grid) grid = static_cast<int>(items);
@@ -742,7 +742,7 @@ int fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float* lse, 
         p.kv.seqused_k = nullptr;
         p.kv.o_part = nullptr;
         p.kv.lse_part = nullptr;
-        p.kv.group = 1;
+        p.group = 1;
         int grid = st->num_sms;
         const int64_t items = static_cast<int64_t>(B) * H * ((Nq + 255) / 256);
         if (items < grid) grid = static_cast<int>(items);
@@ -928,6 +928,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     float* part = static_cast<float*>(workspace);
 
     if (!kv4_direct(Nq, group, Nk)) {
+        if (group > 65535) return FA_ERR_BAD_SHAPE;
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
         const int ns = num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, st->num_sms);

@@ -96,7 +96,6 @@ struct FwdParams {
         const int* seqused_k;   // or nullptr (all Nk rows in use)
         float* o_part;          // [nsplit, B * N, H, D]
         float* lse_part;        // [nsplit, H, B * N], base 2
-        int group;              // query heads to a key/value head (the maps' heads: H / group)
     };
     union {
         F8 f8;
@@ -104,7 +103,10 @@ struct FwdParams {
     };
     union {
         int nb;                 // FP8
-        int nsplit;             // padded cache
+        struct {                // padded cache
+            short nsplit;
+            unsigned short group;   // query heads to a key/value head (the maps' heads: H / group)
+        };
     };
 };
 
@@ -269,7 +271,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                     split = h % p.nsplit;
                     h /= p.nsplit;
                 }
-                [[maybe_unused]] const int hk = kCache ? h / p.kv.group : h;
+                [[maybe_unused]] const int hk = kCache ? h / p.group : h;
                 const SeqSpan sp = sch.span(s);
                 const SeqSpan kp = kCache ? sch.kspan_used(s, p.kv.seqused_k) : sch.kspan(s);
                 const int off = kp.len - sp.len;        // key position of query row 0
