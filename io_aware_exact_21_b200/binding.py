@@ -96,19 +96,17 @@ def status_string(code: int) -> str:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        import torch
         # the handle alone: torch.cuda.current_stream() makes a Stream object
         # around it, which costs as much as the rest of a small call's checks
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -299,15 +297,6 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _fits(t, name, shape, dtype, device, index):
-    """_expect for the calls of a decode step, where the checks are a good part
-    of the time: one look when the tensor is right (index: the CUDA device's),
-    and _expect's message when it is not."""
-    if not (index >= 0 and t is not None and t.shape == shape and t.dtype is dtype
-            and t.get_device() == index and t.is_contiguous()):
-        _expect(t, name, shape, dtype, device)
-
-
 def _expect_bytes(t, name, nbytes, device):
     """A byte buffer (workspace): uint8, dense, at least nbytes long."""
     import torch
@@ -455,45 +444,83 @@ def kv4_cache(B, rows, Hkv, d, device="cuda"):
             torch.zeros((B, Hkv, Nk), dtype=torch.int16, device=device) for n in KV4_NAMES}
 
 
-def _kv4_shape(cache, device, index):
-    """A 4-bit cache's arrays, checked against each other, and (B, Hkv, Nk, d)."""
+def _expect_current(device):
+    """The library launches on the current device and its stream."""
     import torch
-    kc, kw, vc, vw = cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"), cache.get("v_words")
-    _rank(kc, "k_codes", (4,))
-    codes = kc.shape
-    words = codes[:3]
-    _fits(kc, "k_codes", codes, torch.uint8, device, index)
-    _fits(kw, "k_words", words, torch.int16, device, index)
-    _fits(vc, "v_codes", codes, torch.uint8, device, index)
-    _fits(vw, "v_words", words, torch.int16, device, index)
-    # the library launches on the current device and its stream
-    if index >= 0 and index != torch.cuda.current_device():
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
         raise ValueError("the tensors are on %s, the current device is cuda:%d"
                          % (device, torch.cuda.current_device()))
-    return (kc, kw, vc, vw), codes[0], codes[1], codes[2], 2 * codes[3]
 
 
-def _kv4_rows(t, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index):
-    """Checks the rows' side of a write or read; returns its N argument."""
+def _expect_kv4_cache(cache, B, Hkv, d, device):
+    """A 4-bit cache's arrays for B sequences and Hkv heads of d channels."""
     import torch
+    _rank(cache.get("k_codes"), "k_codes", (4,))
+    Nk = cache["k_codes"].shape[2]
+    for n in KV4_NAMES:
+        if n.endswith("codes"):
+            _expect(cache.get(n), n, (B, Hkv, Nk, d // 2), torch.uint8, device)
+        else:
+            _expect(cache.get(n), n, (B, Hkv, Nk), torch.int16, device)
+    _expect_current(device)
+
+
+def _kv4_cache_fits(kc, kw, vc, vw, index):
+    """Whether these are a 4-bit cache's arrays on the current CUDA device
+    `index`: one look at each, for the calls of a decode step, where the checks
+    are a good part of the time.  (_expect_kv4_cache says what does not fit.)"""
+    import torch
+    codes = kc.shape
+    words = codes[:3]
+    return (kc.dtype is torch.uint8 and vc.dtype is torch.uint8 and kw.dtype is torch.int16
+            and vw.dtype is torch.int16 and vc.shape == codes and kw.shape == words and vw.shape == words
+            and kc.is_contiguous() and vc.is_contiguous() and kw.is_contiguous() and vw.is_contiguous()
+            and kc.get_device() == vc.get_device() == kw.get_device() == vw.get_device() == index >= 0
+            and index == torch.cuda.current_device())
+
+
+def _int32_fits(t, n, index):
+    import torch
+    return t is None or (t.dtype is torch.int32 and t.get_device() == index and t.dim() == 1
+                         and t.shape[0] == n and t.is_contiguous())
+
+
+def _kv4_rows(k, v, cache, cu_seqlens, starts, lens):
+    """Checks a write's or read's tensors.  Returns the cache's arrays and (B,
+    N, Hkv, Nk, d)."""
+    import torch
+    kc, kw, vc, vw = (cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"),
+                      cache.get("v_words"))
+    _rank(kc, "k_codes", (4,))
+    _rank(k, "k", (3, 4))
+    B, Hkv, Nk, half = kc.shape
+    d = 2 * half
     if cu_seqlens is None:
-        _rank(t, "k", (4,))
-        N = t.shape[1]
+        N = k.shape[1]
         shape = (B, N, Hkv, d)
     else:
-        if lens is not None:
-            raise ValueError("lens and cu_seqlens exclude each other")
-        _rank(t, "k (packed)", (3,))
-        N = t.shape[0]
+        N = k.shape[0]
         shape = (N, Hkv, d)
-        _fits(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev, index)
-    if starts is not None:
-        _fits(starts, "starts", (B,), torch.int32, dev, index)
-    if lens is not None:
-        _fits(lens, "lens", (B,), torch.int32, dev, index)
-    _fits(t, "k", shape, torch.bfloat16, dev, index)
-    _fits(v, "v", shape, torch.bfloat16, dev, index)
-    return N
+    index = k.get_device()
+    if not (index >= 0 and kw is not None and vc is not None and vw is not None and v is not None
+            and _kv4_cache_fits(kc, kw, vc, vw, index)
+            and k.shape == shape and v.shape == shape and k.dtype is torch.bfloat16
+            and v.dtype is torch.bfloat16 and v.get_device() == index and k.is_contiguous()
+            and v.is_contiguous() and _int32_fits(cu_seqlens, B + 1, index)
+            and _int32_fits(starts, B, index) and _int32_fits(lens, B, index)
+            and (cu_seqlens is None or lens is None)):
+        dev = k.device
+        _expect_kv4_cache(cache, B, Hkv, d, dev)
+        if cu_seqlens is not None:
+            if lens is not None:
+                raise ValueError("lens and cu_seqlens exclude each other")
+            _expect(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+        for t, name in ((starts, "starts"), (lens, "lens")):
+            if t is not None:
+                _expect(t, name, (B,), torch.int32, dev)
+        _expect(k, "k", shape, torch.bfloat16, dev)
+        _expect(v, "v", shape, torch.bfloat16, dev)
+    return kc, kw, vc, vw, B, N, Hkv, Nk, d
 
 
 def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=None):
@@ -502,11 +529,8 @@ def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=No
     CUDA tensor, None for 0), the first ``lens[b]`` rows of each (None for
     all); or packed [T, Hkv, d] with int32 ``cu_seqlens``.  Rows that fall
     outside the cache are left out.  Returns the cache."""
-    _rank(k, "k", (3, 4))
-    dev, index = k.device, k.get_device()
-    arrays, B, Hkv, Nk, d = _kv4_shape(cache, dev, index)
-    N = _kv4_rows(k, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index)
-    _check(fa_quantize_kv4(k, v, *arrays, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
+    kc, kw, vc, vw, B, N, Hkv, Nk, d = _kv4_rows(k, v, cache, cu_seqlens, starts, lens)
+    _check(fa_quantize_kv4(k, v, kc, kw, vc, vw, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
            "fa_quantize_kv4")
     return cache
 
@@ -517,21 +541,22 @@ def dequantize_kv4(cache, rows=None, starts=None, lens=None, cu_seqlens=None, ou
     ``cu_seqlens``; starts and lens as quantize_kv4.  Rows that belong to no
     sequence or fall outside the cache keep what ``out`` holds (zeros when it
     is not given)."""
-    _rank(cache.get("k_codes"), "k_codes", (4,))
-    dev, index = cache["k_codes"].device, cache["k_codes"].get_device()
-    arrays, B, Hkv, Nk, d = _kv4_shape(cache, dev, index)
     if out is None:
         import torch
-        if rows is None and cu_seqlens is not None:
-            raise ValueError("a packed read needs rows or out")
-        n = Nk if rows is None else rows
-        shape = (B, n, Hkv, d) if cu_seqlens is None else (n, Hkv, d)
-        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        _rank(cache.get("k_codes"), "k_codes", (4,))
+        B, Hkv, Nk, half = cache["k_codes"].shape
+        if rows is None:
+            if cu_seqlens is not None:
+                raise ValueError("a packed read needs rows or out")
+            rows = Nk
+        shape = (B, rows, Hkv, 2 * half) if cu_seqlens is None else (rows, Hkv, 2 * half)
+        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=cache["k_codes"].device)
+                    for _ in range(2))
     k, v = out
-    N = _kv4_rows(k, v, B, Hkv, d, cu_seqlens, starts, lens, dev, index)
+    kc, kw, vc, vw, B, N, Hkv, Nk, d = _kv4_rows(k, v, cache, cu_seqlens, starts, lens)
     if rows is not None and rows != N:
         raise ValueError("out holds %d rows, rows is %d" % (N, rows))
-    _check(fa_dequantize_kv4(*arrays, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
+    _check(fa_dequantize_kv4(kc, kw, vc, vw, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
            "fa_dequantize_kv4")
     return k, v
 
@@ -544,32 +569,40 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
     are the last Nq of those positions.  Returns (O, LSE)."""
     import torch
     _rank(q, "q", (4,))
+    kc, kw, vc, vw = (cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"),
+                      cache.get("v_words"))
+    _rank(kc, "k_codes", (4,))
     B, Nq, H, d = shape = q.shape
-    dev, index = q.device, q.get_device()
-    _fits(q, "q", shape, torch.bfloat16, dev, index)
-    arrays, cB, Hkv, Nk, cd = _kv4_shape(cache, dev, index)
-    if cB != B or cd != d:
-        raise ValueError("the cache holds %d sequences of d = %d, q has %d of %d" % (cB, cd, B, d))
+    cB, Hkv, Nk, half = kc.shape
+    index = q.get_device()
+    if not (index >= 0 and kw is not None and vc is not None and vw is not None
+            and _kv4_cache_fits(kc, kw, vc, vw, index) and q.dtype is torch.bfloat16 and q.is_contiguous()
+            and _int32_fits(seqlens_k, B, index)):
+        dev = q.device
+        _expect(q, "q", shape, torch.bfloat16, dev)
+        _expect_kv4_cache(cache, cB, Hkv, 2 * half, dev)
+        if seqlens_k is not None:
+            _expect(seqlens_k, "seqlens_k", (B,), torch.int32, dev)
+    if cB != B or 2 * half != d:
+        raise ValueError("the cache holds %d sequences of d = %d, q has %d of %d" % (cB, 2 * half, B, d))
     if Hkv == 0 or H % Hkv:
         raise ValueError("q has %d heads, not a multiple of the cache's %d" % (H, Hkv))
-    if seqlens_k is not None:
-        _fits(seqlens_k, "seqlens_k", (B,), torch.int32, dev, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _fits(out, "out", shape, torch.bfloat16, dev, index)
+        _expect(out, "out", shape, torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, H, Nq), dtype=torch.float32)
     else:
-        _fits(lse, "lse", (B, H, Nq), torch.float32, dev, index)
+        _expect(lse, "lse", (B, H, Nq), torch.float32, q.device)
     need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
     if workspace is not None:
-        _expect_bytes(workspace, "workspace", need, dev)
+        _expect_bytes(workspace, "workspace", need, q.device)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(fa_fwd_kv4(q, *arrays, out, lse, B, H, Hkv, Nq, Nk, d, scale, causal, window, seqlens_k,
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    _check(fa_fwd_kv4(q, kc, kw, vc, vw, out, lse, B, H, Hkv, Nq, Nk, d, scale, causal, window, seqlens_k,
                       num_splits, workspace, 0 if workspace is None else workspace.numel(), stream),
            "fa_fwd_kv4")
     return out, lse
