@@ -226,7 +226,8 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * queries are the last Nq of those positions, and rows past nk_b are never
  * used.  Queries without a key get O = 0, LSE = -inf.  A row whose K or V
  * stands for NaN makes O NaN (and LSE unspecified) for the queries that see
- * it, and reaches no others.
+ * it, and reaches no others.  Elements of q are below 2^116 in magnitude (or
+ * O of their query is unspecified).
  *   Few query rows to a key/value head (Nq * H / Hkv; up to 96 with a head
  * each, 192 with four to a head) run on kernels that multiply the 4-bit codes
  * as they are; more are run by reading the rows in use back into the workspace
@@ -422,7 +423,8 @@ int fa_profile_cta_balance(double* balance, int* ctas);
  * consumer's bounded wait runs out after timeout_ns nanoseconds (0 keeps the
  * default of 2 s) and the kernel returns with FA_ERR_DEVICE_TIMEOUT recorded.
  * mode 2: the same for the decode kernel of fa_fwd_kvcache (queries <= 16):
- * each CTA's load thread leaves its first K/V stage unloaded.
+ * each CTA's load thread leaves its first K/V stage unloaded.  mode 3: the same
+ * for fa_fwd_kv4 with few query rows: each warp leaves its first K tile unloaded.
  * Host-side setting, not thread safe; returns the previous mode.
  */
 int fa_debug_set_fault(int mode, unsigned long long timeout_ns);

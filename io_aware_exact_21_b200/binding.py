@@ -170,13 +170,15 @@ def fa_dequantize_kv4(k_codes, k_words, v_codes, v_words, k, v, B, N, Hkv, Nk, d
 def fa_fwd_kv4(q, k_codes, k_words, v_codes, v_words, o, lse, B, H, Hkv, Nq, Nk, d, scale, causal,
                window, seqlens_k, num_splits, workspace, workspace_bytes, stream=None) -> int:
     return load_library().fa_fwd_kv4(_ptr(q), _ptr(k_codes), _ptr(k_words), _ptr(v_codes),
-                                     _ptr(v_words), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d, scale,
-                                     causal, window, _ptr(seqlens_k), num_splits, _ptr(workspace),
-                                     workspace_bytes, _stream(stream))
+                                     _ptr(v_words), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d,
+                                     float(scale), int(causal), int(window), _ptr(seqlens_k),
+                                     int(num_splits), _ptr(workspace), workspace_bytes,
+                                     _stream(stream))
 
 
 def fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits) -> int:
-    return load_library().fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
+    return load_library().fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, int(window),
+                                                    int(num_splits))
 
 
 def fa_fp8_vt_bytes(B, H, N, d) -> int:

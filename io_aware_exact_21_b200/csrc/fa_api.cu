@@ -899,7 +899,6 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
                const void* v_words, void* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
                float scale, int causal, int window, const int* seqlens_k, int num_splits,
                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    if (!q || !o || !lse) return FA_ERR_NULLPTR;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
     if (H <= 0 || Nq < 0 || kv4_bad_cache(B, Hkv, Nk, d) || H % Hkv != 0) return FA_ERR_BAD_SHAPE;
     if (num_splits < 0 || num_splits > fa::kDecMaxSplits) return FA_ERR_BAD_SHAPE;
@@ -913,6 +912,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         (kv4_direct(Nq, group, Nk) && static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
                                           (int64_t{1} << 31) - 1))      // its key tiles are counted in 32 bits
         return FA_ERR_BAD_SHAPE;
+    if (rows_q > 0 && (!q || !o || !lse)) return FA_ERR_NULLPTR;
     if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
     if (misaligned(q) || misaligned(k_codes) || misaligned(k_words) || misaligned(v_codes) ||
         misaligned(v_words) || misaligned(o) || misaligned(lse) ||
@@ -984,6 +984,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.scale_log2 = scale * 1.4426950408889634f;
     p.error_word = st->error_word;
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
+    p.fault_skip = g_fault_mode == 3 ? 1 : 0;
     if (d == 64)
         return kv4_block_rows(rows) == 8 ? launch_kv4_decode<64, 1>(p, plan, stream) : launch_kv4_decode<64, 2>(p, plan, stream);
     return kv4_block_rows(rows) == 8 ? launch_kv4_decode<128, 1>(p, plan, stream) : launch_kv4_decode<128, 2>(p, plan, stream);

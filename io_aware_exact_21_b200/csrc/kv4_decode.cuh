@@ -21,17 +21,28 @@
 // bf16's 2^-8).  Everything else is fp32, the row sums take the unrounded p.
 //
 // What bounds it: with R = Nq * H / Hkv query rows to a key/value head the
-// cache is D + 4 bytes a token and head for 4 R D operations, so up to a few
-// dozen rows HBM is the limit if the instructions per code stay few.  mma.sync
+// cache is D + 4 bytes a token and head for 4 R D operations, so up to a dozen
+// rows HBM is the limit if the instructions per code stay few.  mma.sync
 // rather than tcgen05: its operands come from registers, where the codes are
 // unpacked, while tcgen05 would have them written back to shared or tensor
 // memory as 16-bit words first, four times the cache's bytes.
 //
-// The key tiles of all heads and sequences are cut into equal ranges, one a
-// warp (kv4_span below).  A warp is on its own: it takes its tiles through its
-// own ring of bulk copies, with its own reference and sums, so nothing in the
-// kernel waits for another warp; the partial results of an item that lies in
-// several ranges are merged by kv4_merge_kernel.
+// A warp takes whole key tiles, through its own stage of bulk copies, with its
+// own reference and sums, and waits for no other warp; what several warps have
+// of the same rows is put together at the end, within a cluster
+// (kv4_cluster_kernel) or by a second kernel (kv4_decode_kernel and
+// kv4_merge_kernel).
+//
+// Measured on one B200 at 16 requests x 16 heads, one query each, caches of
+// 4096 to 8192 rows, d = 128 (208 MB, 31.7 us at the measured copy rate): 43 us
+// with the merge, which is 3 of them.  The same with the arithmetic left out 34
+// us, with the loads left out 33 us; so both sides matter, and an instruction
+// less a code has been worth more than anything else: 64 us with a tile of 32
+// keys, cp.async and a maximum looked for in each tile; 47 us with equal ranges
+// and the maximum only where a tile's sum asks for it; 45 us with ldmatrix in
+// place of byte permutes.  More warps with fewer registers (16 of 128 an SM:
+// 46 us against 43 without the merge), deeper stages (44 against 43) and 8-bit
+// products (their mma.sync is slower here than the 16-bit one) did not pay.
 //
 // Per tile: S^T = C^k q^T with 16 keys x 8 query rows to an mma (the codes are
 // the A operand), p from it in registers, transposed by movmatrix into the B
@@ -62,6 +73,7 @@ struct Kv4DecodeParams {
     float scale_log2;
     int* error_word;
     uint64_t timeout_ns;
+    int fault_skip;              // test hook: the first K tile of each warp is left unloaded
 };
 
 template <int D, int NT>
@@ -247,7 +259,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
                           ((((v_key % KPL) * (8 / KPL)) | (lane >> 4)) ^ (v_key / KPL)) * 16;
     const int kkey = kv4_key(g8);
     if (count > 0) {
-        load_k(0);
+        if (!p.fault_skip) load_k(0);
         load_v(0);
     }
 
@@ -385,108 +397,108 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         // reference moves to their maximum, and p is taken anew.
         float2 e[C::MT][NT][2], ts[NT];
         for (bool move = false;; move = true) {
-        float2 (&s)[C::MT][NT][2] = e;
-        // ---- S^T = C^k q^T: keys x 8 NT rows
+            float2 (&s)[C::MT][NT][2] = e;
+            // ---- S^T = C^k q^T: keys x 8 NT rows
 #pragma unroll
-        for (int m = 0; m < C::MT; ++m) {
-            uint32_t ka[W], kb[W];
-            const uint8_t* ra = st + (m * 16 + kkey) * C::ROWB + t4 * (W * 4);
-            const uint8_t* rb = ra + 4 * C::ROWB;
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
-                ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
-                kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(rb);
-                ka[0] = u.x; ka[1] = u.y;
-                kb[0] = v.x; kb[1] = v.y;
-            }
+            for (int m = 0; m < C::MT; ++m) {
+                uint32_t ka[W], kb[W];
+                const uint8_t* ra = st + (m * 16 + kkey) * C::ROWB + t4 * (W * 4);
+                const uint8_t* rb = ra + 4 * C::ROWB;
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(rb);
+                    ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+                    kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(rb);
+                    ka[0] = u.x; ka[1] = u.y;
+                    kb[0] = v.x; kb[1] = v.y;
+                }
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const uint32_t u = ka[w], v = kb[w], u8 = u >> 8, v8 = v >> 8;
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t u = ka[w], v = kb[w], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (w == 0)
-                        mma_f16_first(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
-                                      qf[nt][w][0][1]);
-                    else
-                        mma_f16(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
-                                qf[nt][w][0][1]);
-                    mma_f16(s[m][nt], u8 & kNibLo, v8 & kNibLo, u8 & kNibHi, v8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (w == 0)
+                            mma_f16_first(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                          qf[nt][w][0][1]);
+                        else
+                            mma_f16(s[m][nt], u & kNibLo, v & kNibLo, u & kNibHi, v & kNibHi, qf[nt][w][0][0],
+                                    qf[nt][w][0][1]);
+                        mma_f16(s[m][nt], u8 & kNibLo, v8 & kNibLo, u8 & kNibHi, v8 & kNibHi, qf[nt][w][1][0], qf[nt][w][1][1]);
+                    }
                 }
             }
-        }
-        // ---- scores (over the row factor rf) and masks
-#pragma unroll
-        for (int m = 0; m < C::MT; ++m)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float2 sz = sck[m * 16 + half * 4 + kkey];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
-                                           make_float2(sz.x, sz.x));
-            }
-        if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
+            // ---- scores (over the row factor rf) and masks
 #pragma unroll
             for (int m = 0; m < C::MT; ++m)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int key = k0 + m * 16 + half * 4 + kkey;
+                    const float2 sz = sck[m * 16 + half * 4 + kkey];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
-                        if (key >= hi[nt][1] || key < lo[nt][1]) s[m][nt][half].y = kNegInf;
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
+                                               make_float2(sz.x, sz.x));
                 }
-        }
-
-        if (move) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float2 mx = s[0][nt][0];
+            if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
 #pragma unroll
                 for (int m = 0; m < C::MT; ++m)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        mx.x = fmaxf(mx.x, s[m][nt][half].x);
-                        mx.y = fmaxf(mx.y, s[m][nt][half].y);
+                        const int key = k0 + m * 16 + half * 4 + kkey;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (key >= hi[nt][0] || key < lo[nt][0]) s[m][nt][half].x = kNegInf;
+                            if (key >= hi[nt][1] || key < lo[nt][1]) s[m][nt][half].y = kNegInf;
+                        }
                     }
+            }
+
+            if (move) {
 #pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) {
-                    mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
-                    mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
-                }
-                // the reference never falls; -inf (nothing yet) leaves none
-                float2 n2 = fmul2(mx, make_float2(-rf[nt].x, -rf[nt].y));
-                n2 = make_float2(fminf(n2.x, nm[nt].x), fminf(n2.y, nm[nt].y));
-                const float2 a = make_float2(nm[nt].x == kNoRef ? 0.f : ex2(n2.x - nm[nt].x),
-                                             nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
-                nm[nt] = n2;
-                l[nt] = fmul2(l[nt], a);
-                za[nt] = fmul2(za[nt], a);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float2 mx = s[0][nt][0];
 #pragma unroll
-                for (int m = 0; m < D / 16; ++m) {
-                    oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
-                    oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
+                    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            mx.x = fmaxf(mx.x, s[m][nt][half].x);
+                            mx.y = fmaxf(mx.y, s[m][nt][half].y);
+                        }
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+                        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+                    }
+                    // the reference never falls; -inf (nothing yet) leaves none
+                    float2 n2 = fmul2(mx, make_float2(-rf[nt].x, -rf[nt].y));
+                    n2 = make_float2(fminf(n2.x, nm[nt].x), fminf(n2.y, nm[nt].y));
+                    const float2 a = make_float2(nm[nt].x == kNoRef ? 0.f : ex2(n2.x - nm[nt].x),
+                                                 nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
+                    nm[nt] = n2;
+                    l[nt] = fmul2(l[nt], a);
+                    za[nt] = fmul2(za[nt], a);
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
+                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
+                    }
                 }
             }
-        }
-        bool over = false;
+            bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            ts[nt] = make_float2(0.f, 0.f);
+            for (int nt = 0; nt < NT; ++nt) {
+                ts[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int m = 0; m < C::MT; ++m)
+                for (int m = 0; m < C::MT; ++m)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
-                    e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
-                    ts[nt] = fadd2(ts[nt], e[m][nt][half]);
-                }
-            over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
-        }
-        if (move || !__any_sync(0xffffffffu, over)) break;
+                    for (int half = 0; half < 2; ++half) {
+                        const float2 y = ffma2(s[m][nt][half], rf[nt], nm[nt]);
+                        e[m][nt][half] = make_float2(ex2(y.x), ex2(y.y));
+                        ts[nt] = fadd2(ts[nt], e[m][nt][half]);
+                    }
+                over = over || ts[nt].x > kKv4Over || ts[nt].y > kKv4Over;
+            }
+            if (move || !__any_sync(0xffffffffu, over)) break;
         }
         __syncwarp();               // K may be loaded again
         if (i + 1 < count) load_k(i + 1);

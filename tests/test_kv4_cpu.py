@@ -57,7 +57,7 @@ def attend_args(**kw):
     (dict(Nq=100), -6), (dict(Nq=100, workspace=P, workspace_bytes=1000), -6),
     (dict(num_splits=0, Nk=65536), -6),
     (dict(scale=0.0), -9), (dict(scale=float("nan")), -9),
-    (dict(Nq=0), 0), (dict(B=0), 0),
+    (dict(Nq=0), 0), (dict(B=0), 0), (dict(Nq=0, q=None, o=None, lse=None), 0),
 ])
 def test_attention_validation(kw, code):
     assert fa.fa_fwd_kv4(**attend_args(**kw)) == code

@@ -596,3 +596,59 @@ def test_separate_streams():
         o2, lse2 = fa.forward_kv4(q, cache, causal=True)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
+
+
+def test_nothing_to_do():
+    cache = random_cache(2, 64, 2, 64, seed=15)
+    o, lse = fa.forward_kv4(queries(2, 0, 4, 64, 1), cache)
+    assert o.shape == (2, 0, 4, 64) and lse.shape == (2, 4, 0)
+    empty = fa.kv4_cache(0, 64, 2, 64)
+    assert fa.forward_kv4(queries(0, 1, 4, 64, 1), empty)[0].shape == (0, 1, 4, 64)
+    before = {n: t.clone() for n, t in cache.items()}
+    none = torch.empty((2, 0, 2, 64), dtype=torch.bfloat16, device=DEV)
+    fa.quantize_kv4(none, none, cache)
+    fa.quantize_kv4(queries(2, 3, 2, 64, 1), queries(2, 3, 2, 64, 2), cache,
+                    lens=torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert all(torch.equal(cache[n], before[n]) for n in cache)
+
+
+@pytest.mark.parametrize("num_splits", [0, 4])
+def test_a_wait_that_runs_out_is_reported(num_splits):
+    # each warp's first K tile is left unloaded: the waits end, the host reads
+    # the status, and the next call works
+    cache = random_cache(2, 512, 2, 128, seed=16)
+    q = queries(2, 1, 4, 128, 1)
+    want, _ = fa.forward_kv4(q, cache, causal=True, num_splits=num_splits)
+    torch.cuda.synchronize()
+    assert fa.fa_debug_set_fault(3, 1000000) == 0
+    try:
+        fa.forward_kv4(q, cache, causal=True, num_splits=num_splits)
+        assert fa.fa_get_device_error() == -8
+    finally:
+        assert fa.fa_debug_set_fault(0, 0) == 3
+    o, _ = fa.forward_kv4(q, cache, causal=True, num_splits=num_splits)
+    assert fa.fa_get_device_error() == 0 and torch.equal(o, want)
+
+
+def test_lengths_of_many_sequences():
+    # more sequences than a CTA has threads, most of them short or empty
+    B, Hkv, d, Nk = 300, 1, 64, 72
+    cache = random_cache(B, Nk, Hkv, d, seed=17)
+    lens = some_lens(B, Nk, 3)
+    lens[::3] = 0
+    lens[100:180] = 0
+    q = queries(B, 1, 2, d, 4)
+    for ns in (0, 1, 7):
+        check(q, {n: t.clone() for n, t in cache.items()}, lens, True, 0, ns)
+    check(q, {n: t.clone() for n, t in cache.items()}, torch.zeros(B, dtype=torch.int32), True, 0, 3)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    # the library launches on the current device: tensors elsewhere are refused
+    cache = random_cache(1, 64, 1, 64, seed=18)
+    q = queries(1, 1, 1, 64, 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: fa.forward_kv4(q, cache), lambda: fa.dequantize_kv4(cache),
+                 lambda: fa.quantize_kv4(q, q, cache)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
