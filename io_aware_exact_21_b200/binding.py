@@ -68,6 +68,16 @@ class FaError(RuntimeError):
 
 
 _lib = None
+_torch_module = None
+
+
+def _torch():
+    """The torch module, imported by the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def library_path() -> str:
@@ -105,8 +115,8 @@ def _stream(stream):
     if stream is None:
         # the handle alone: torch.cuda.current_stream() makes a Stream object
         # around it, which costs as much as the rest of a small call's checks
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -467,62 +477,64 @@ def _expect_kv4_cache(cache, B, Hkv, d, device):
     _expect_current(device)
 
 
-def _kv4_cache_fits(kc, kw, vc, vw, index):
-    """Whether these are a 4-bit cache's arrays on the current CUDA device
-    `index`: one look at each, for the calls of a decode step, where the checks
-    are a good part of the time.  (_expect_kv4_cache says what does not fit.)"""
-    import torch
+# The calls of a decode step are short, and their checks are a good part of the
+# time: what fits is seen in one look (below), and only what does not goes
+# through the _expect functions, which say why.
+
+def _kv4_cache_fits(torch, kc, kw, vc, vw, index):
+    """Whether these are a 4-bit cache's arrays on the current CUDA device `index`."""
+    if kc is None or kw is None or vc is None or vw is None:
+        return False
     codes = kc.shape
     words = codes[:3]
-    return (kc.dtype is torch.uint8 and vc.dtype is torch.uint8 and kw.dtype is torch.int16
-            and vw.dtype is torch.int16 and vc.shape == codes and kw.shape == words and vw.shape == words
+    return (len(codes) == 4 and kc.dtype is torch.uint8 and vc.dtype is torch.uint8
+            and kw.dtype is torch.int16 and vw.dtype is torch.int16 and vc.shape == codes
+            and kw.shape == words and vw.shape == words
             and kc.is_contiguous() and vc.is_contiguous() and kw.is_contiguous() and vw.is_contiguous()
-            and kc.get_device() == vc.get_device() == kw.get_device() == vw.get_device() == index >= 0
+            and kc.get_device() == vc.get_device() == kw.get_device() == vw.get_device() == index
             and index == torch.cuda.current_device())
 
 
-def _int32_fits(t, n, index):
-    import torch
-    return t is None or (t.dtype is torch.int32 and t.get_device() == index and t.dim() == 1
-                         and t.shape[0] == n and t.is_contiguous())
+def _int32_fits(torch, t, n, index):
+    return (t.dtype is torch.int32 and t.get_device() == index and t.dim() == 1 and t.shape[0] == n
+            and t.is_contiguous())
 
 
 def _kv4_rows(k, v, cache, cu_seqlens, starts, lens):
     """Checks a write's or read's tensors.  Returns the cache's arrays and (B,
     N, Hkv, Nk, d)."""
-    import torch
+    torch = _torch()
     kc, kw, vc, vw = (cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"),
                       cache.get("v_words"))
+    index = -1 if k is None else k.get_device()
+    if index >= 0 and v is not None and _kv4_cache_fits(torch, kc, kw, vc, vw, index):
+        B, Hkv, Nk, half = kc.shape
+        shape = k.shape
+        if (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and v.shape == shape
+                and v.get_device() == index and k.is_contiguous() and v.is_contiguous()
+                and shape[-2:] == (Hkv, 2 * half)
+                and (len(shape) == 4 and shape[0] == B if cu_seqlens is None else
+                     len(shape) == 3 and lens is None and _int32_fits(torch, cu_seqlens, B + 1, index))
+                and (starts is None or _int32_fits(torch, starts, B, index))
+                and (lens is None or _int32_fits(torch, lens, B, index))):
+            return kc, kw, vc, vw, B, shape[-3], Hkv, Nk, 2 * half
     _rank(kc, "k_codes", (4,))
-    _rank(k, "k", (3, 4))
+    _rank(k, "k", (4,) if cu_seqlens is None else (3,))
     B, Hkv, Nk, half = kc.shape
-    d = 2 * half
-    if cu_seqlens is None:
-        N = k.shape[1]
-        shape = (B, N, Hkv, d)
-    else:
-        N = k.shape[0]
-        shape = (N, Hkv, d)
-    index = k.get_device()
-    if not (index >= 0 and kw is not None and vc is not None and vw is not None and v is not None
-            and _kv4_cache_fits(kc, kw, vc, vw, index)
-            and k.shape == shape and v.shape == shape and k.dtype is torch.bfloat16
-            and v.dtype is torch.bfloat16 and v.get_device() == index and k.is_contiguous()
-            and v.is_contiguous() and _int32_fits(cu_seqlens, B + 1, index)
-            and _int32_fits(starts, B, index) and _int32_fits(lens, B, index)
-            and (cu_seqlens is None or lens is None)):
-        dev = k.device
-        _expect_kv4_cache(cache, B, Hkv, d, dev)
-        if cu_seqlens is not None:
-            if lens is not None:
-                raise ValueError("lens and cu_seqlens exclude each other")
-            _expect(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
-        for t, name in ((starts, "starts"), (lens, "lens")):
-            if t is not None:
-                _expect(t, name, (B,), torch.int32, dev)
-        _expect(k, "k", shape, torch.bfloat16, dev)
-        _expect(v, "v", shape, torch.bfloat16, dev)
-    return kc, kw, vc, vw, B, N, Hkv, Nk, d
+    N = k.shape[-3]
+    shape = (B, N, Hkv, 2 * half) if cu_seqlens is None else (N, Hkv, 2 * half)
+    dev = k.device
+    _expect_kv4_cache(cache, B, Hkv, 2 * half, dev)
+    if cu_seqlens is not None:
+        if lens is not None:
+            raise ValueError("lens and cu_seqlens exclude each other")
+        _expect(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    for t, name in ((starts, "starts"), (lens, "lens")):
+        if t is not None:
+            _expect(t, name, (B,), torch.int32, dev)
+    _expect(k, "k", shape, torch.bfloat16, dev)
+    _expect(v, "v", shape, torch.bfloat16, dev)
+    return kc, kw, vc, vw, B, N, Hkv, Nk, 2 * half
 
 
 def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=None):
@@ -569,22 +581,22 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
     the cache's Hkv (query head h reads head h // (H // Hkv)); sequence b uses
     its first seqlens_k[b] rows (int32 CUDA tensor, or None for all), queries
     are the last Nq of those positions.  Returns (O, LSE)."""
-    import torch
-    _rank(q, "q", (4,))
+    torch = _torch()
     kc, kw, vc, vw = (cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"),
                       cache.get("v_words"))
-    _rank(kc, "k_codes", (4,))
+    index = -1 if q is None else q.get_device()
+    fits = index >= 0 and q.dim() == 4 and q.dtype is torch.bfloat16 and q.is_contiguous() \
+        and _kv4_cache_fits(torch, kc, kw, vc, vw, index) \
+        and (seqlens_k is None or _int32_fits(torch, seqlens_k, q.shape[0], index))
+    if not fits:
+        _rank(q, "q", (4,))
+        _rank(kc, "k_codes", (4,))
+        _expect(q, "q", q.shape, torch.bfloat16, q.device)
+        _expect_kv4_cache(cache, kc.shape[0], kc.shape[1], 2 * kc.shape[3], q.device)
+        if seqlens_k is not None:
+            _expect(seqlens_k, "seqlens_k", (q.shape[0],), torch.int32, q.device)
     B, Nq, H, d = shape = q.shape
     cB, Hkv, Nk, half = kc.shape
-    index = q.get_device()
-    if not (index >= 0 and kw is not None and vc is not None and vw is not None
-            and _kv4_cache_fits(kc, kw, vc, vw, index) and q.dtype is torch.bfloat16 and q.is_contiguous()
-            and _int32_fits(seqlens_k, B, index)):
-        dev = q.device
-        _expect(q, "q", shape, torch.bfloat16, dev)
-        _expect_kv4_cache(cache, cB, Hkv, 2 * half, dev)
-        if seqlens_k is not None:
-            _expect(seqlens_k, "seqlens_k", (B,), torch.int32, dev)
     if cB != B or 2 * half != d:
         raise ValueError("the cache holds %d sequences of d = %d, q has %d of %d" % (cB, 2 * half, B, d))
     if Hkv == 0 or H % Hkv:
