@@ -458,6 +458,14 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
 }
 
 // ------------------------------------------------------ 4-bit K/V cache --
+// Query rows a CTA of kv4_decode_kernel holds: 8 or 16.
+int kv4_block_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+int64_t kv4_row_blocks(int64_t rows) {
+    const int per = kv4_block_rows(rows);
+    return (rows + per - 1) / per;
+}
+
 // Whether attention over the 4-bit cache multiplies the codes as they are, 16
 // query rows to a warp, or reads the rows back for the forward, whose blocks
 // hold 256 queries of one head.  The one's time goes with the rows, Nq * group;
@@ -466,17 +474,22 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
 // 8192 rows, d 128: group 1 and 64 queries 120 / 257; group 4 and 32 queries
 // 226 / 525, 64 queries 429 / 527; B 32, 2 kv heads, 1000 rows, d 64, group 4:
 // 16 queries 14 / 44, 64 queries 54 / 44.
-bool kv4_direct(int Nq, int group, int Nk) {
-    const int64_t blocks = static_cast<int64_t>(group) * ((Nq + 255) / 256);
-    return static_cast<int64_t>(Nq) * group <= 64 + 32 * blocks || Nk == 0;
-}
-
-// Query rows a CTA of kv4_decode_kernel holds: 8 or 16.
-int kv4_block_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
-
-int64_t kv4_row_blocks(int64_t rows) {
-    const int per = kv4_block_rows(rows);
-    return (rows + per - 1) / per;
+// The read-back's three launches cost 20 us or so besides, in which the codes'
+// kernel does 32 passes of 16 rows over a tile of 64 keys on each SM; while its
+// items all run at once the limit grows by that.  There, d 128: B 2, 4 kv heads,
+// 4096 rows: group 1 and 200 queries 25 / 32, 512 queries 47 / 35; group 4 and
+// 50 queries 25 / 29, 100 queries 36 / 31; B 1, 8 kv heads, 2000 rows, group 1:
+// 100 queries 15 / 30, 512 queries 37 / 34.  Where not all run at once, B 4, 8 kv
+// heads, 1024 rows, group 1 and 200 queries 36 / 28.
+bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int num_sms) {
+    using C = fa::Kv4DecCfg<128, 2>;
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    int64_t limit = 64 + 32 * static_cast<int64_t>(group) * ((Nq + 255) / 256);
+    const int64_t heads = static_cast<int64_t>(B) * Hkv;
+    if (rows <= limit || Nk == 0 || heads == 0) return true;
+    if (heads * kv4_row_blocks(rows) <= static_cast<int64_t>(num_sms) * C::MIN_CTAS)
+        limit += static_cast<int64_t>(num_sms) * 32 * 16 / (heads * ((Nk + C::BN - 1) / C::BN));
+    return rows <= limit;
 }
 
 // How the key tiles are dealt out: to a cluster of `cluster` CTAs each item
@@ -524,7 +537,7 @@ size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
 // maximum and sum), or of a chunk's splits.
 size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const int group = H / Hkv;
-    if (!kv4_direct(Nq, group, Nk))
+    if (!kv4_direct(B, Hkv, Nq, group, Nk, num_sms))
         return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
     const size_t rows = 2 * static_cast<size_t>(kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms).ranges) *
                         kv4_block_rows(static_cast<int64_t>(Nq) * group);
@@ -533,7 +546,7 @@ size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, 
 
 size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
-    return kv4_direct(Nq, H / Hkv, Nk) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
+    return kv4_direct(B, Hkv, Nq, H / Hkv, Nk, num_sms) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
 }
 
 bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
@@ -908,9 +921,13 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     const int64_t rows_k = static_cast<int64_t>(B) * Nk;
     const int group = H / Hkv;
     if (rows_q > (int64_t{1} << 31) - 1 || rows_q * H * d > (int64_t{1} << 40) ||
-        (kv4_direct(Nq, group, Nk) && rows_q * H > (int64_t{1} << 31) - 1) ||
-        (kv4_direct(Nq, group, Nk) && static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
-                                          (int64_t{1} << 31) - 1))      // its key tiles are counted in 32 bits
+        static_cast<int64_t>(Nq) * group > (int64_t{1} << 31) - 1)
+        return FA_ERR_BAD_SHAPE;
+    const int num_sms = current_sms();
+    const bool direct = kv4_direct(B, Hkv, Nq, group, Nk, num_sms);
+    if (direct && (rows_q * H > (int64_t{1} << 31) - 1 ||           // its key tiles are counted in 32 bits
+                   static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
+                       (int64_t{1} << 31) - 1))
         return FA_ERR_BAD_SHAPE;
     if (rows_q > 0 && (!q || !o || !lse)) return FA_ERR_NULLPTR;
     if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
@@ -919,7 +936,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
         return FA_ERR_MISALIGNED;
     if (rows_q == 0) return FA_OK;
-    const size_t need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits);
+    const size_t need = kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
     if (need > 0 && misaligned(workspace)) return FA_ERR_MISALIGNED;
     DeviceState* st = nullptr;
@@ -927,7 +944,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     if (rc != FA_OK) return rc;
     float* part = static_cast<float*>(workspace);
 
-    if (!kv4_direct(Nq, group, Nk)) {
+    if (!direct) {
         if (group > 65535) return FA_ERR_BAD_SHAPE;
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
