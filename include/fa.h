@@ -229,16 +229,16 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * it, and reaches no others.  Elements of q are below 2^116 in magnitude (or
  * O of their query is unspecified).
  *   Few query rows to a key/value head (Nq * H / Hkv; up to 96 with a head
- * each, 192 with four to a head) run on kernels that multiply the 4-bit codes
- * as they are; more are run by reading the rows in use back into the workspace
- * for the tensor-core forward.
+ * each, 192 with four to a head, more where the whole problem is small) run on
+ * kernels that multiply the 4-bit codes as they are; more are run by reading
+ * the rows in use back into the workspace for the tensor-core forward.
  *   num_splits : few rows: the keys of all sequences and heads together are
  * cut into equal ranges, num_splits to each (sequence, key/value head) on
  * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.
  *   workspace : fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window,
- * num_splits) bytes (for num_splits = 0 they are those of the current device;
- * where they are 0 it may be NULL), 16-byte aligned; contents on entry do not matter.  Calls that may overlap on the GPU
- * need one each.
+ * num_splits) bytes (for the current device; 0 for a shape that fa_fwd_kv4
+ * refuses; where they are 0 it may be NULL), 16-byte aligned; contents on
+ * entry do not matter.  Calls that may overlap on the GPU need one each.
  * Errors as fa_fwd_kvcache; H not a multiple of Hkv is FA_ERR_BAD_SHAPE.
  */
 int fa_quantize_kv4(const void* k, const void* v, void* k_codes, void* k_words, void* v_codes,

@@ -487,7 +487,8 @@ bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int num_sms) {
     int64_t limit = 64 + 32 * static_cast<int64_t>(group) * ((Nq + 255) / 256);
     const int64_t heads = static_cast<int64_t>(B) * Hkv;
     if (rows <= limit || Nk == 0 || heads == 0) return true;
-    if (heads * kv4_row_blocks(rows) <= static_cast<int64_t>(num_sms) * C::MIN_CTAS)
+    const int64_t slots = static_cast<int64_t>(num_sms) * C::MIN_CTAS;
+    if (heads <= slots && heads * kv4_row_blocks(rows) <= slots)
         limit += static_cast<int64_t>(num_sms) * 32 * 16 / (heads * ((Nk + C::BN - 1) / C::BN));
     return rows <= limit;
 }
@@ -552,7 +553,19 @@ size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int win
 bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
     return B < 0 || Hkv <= 0 || Nk < 0 || Nk % 8 != 0 ||
            static_cast<int64_t>(B) * Nk > (int64_t{1} << 31) - 1 ||
-           static_cast<int64_t>(B) * Nk * Hkv * d > (int64_t{1} << 40);
+           static_cast<int64_t>(B) * Nk * Hkv > (int64_t{1} << 40) / d;
+}
+
+// Shapes that fa_fwd_kv4 refuses.
+bool kv4_bad_attention(int B, int H, int Hkv, int Nq, int Nk, int d, int num_sms) {
+    constexpr int64_t kMax = (int64_t{1} << 31) - 1;
+    if (H <= 0 || Nq < 0 || kv4_bad_cache(B, Hkv, Nk, d) || H % Hkv != 0) return true;
+    const int64_t rows_q = static_cast<int64_t>(B) * Nq, rows = static_cast<int64_t>(Nq) * (H / Hkv);
+    if (rows_q > kMax || rows_q * H > (int64_t{1} << 40) / d || rows > kMax) return true;
+    if (rows_q == 0) return false;
+    if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, num_sms)) return H / Hkv > 65535;
+    return rows_q * H > kMax ||      // a CTA each in the merge; the key tiles are counted in 32 bits
+           static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(rows) > kMax;
 }
 
 // Writes (kWrite) or reads the rows of p.place, K and V in one launch.
@@ -904,8 +917,11 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
 }
 
 size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits) {
-    if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || Nq <= 0 || Nk < 0 || d <= 0 || num_splits < 0) return 0;
-    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, current_sms());
+    const int num_sms = current_sms();
+    if ((d != 64 && d != 128) || num_splits < 0 || num_splits > fa::kDecMaxSplits ||
+        kv4_bad_attention(B, H, Hkv, Nq, Nk, d, num_sms) || B == 0 || Nq == 0)
+        return 0;
+    return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
 }
 
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const void* v_codes,
@@ -913,22 +929,15 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
                float scale, int causal, int window, const int* seqlens_k, int num_splits,
                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
-    if (H <= 0 || Nq < 0 || kv4_bad_cache(B, Hkv, Nk, d) || H % Hkv != 0) return FA_ERR_BAD_SHAPE;
+    const int num_sms = current_sms();
+    if (kv4_bad_attention(B, H, Hkv, Nq, Nk, d, num_sms)) return FA_ERR_BAD_SHAPE;
     if (num_splits < 0 || num_splits > fa::kDecMaxSplits) return FA_ERR_BAD_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_BAD_SCALE;
     if (window > 0 && !causal) return FA_ERR_BAD_MASK;
+    if (window >= Nk) window = 0;           // as wide as the cache: no window
     const int64_t rows_q = static_cast<int64_t>(B) * Nq;
     const int64_t rows_k = static_cast<int64_t>(B) * Nk;
     const int group = H / Hkv;
-    if (rows_q > (int64_t{1} << 31) - 1 || rows_q * H * d > (int64_t{1} << 40) ||
-        static_cast<int64_t>(Nq) * group > (int64_t{1} << 31) - 1)
-        return FA_ERR_BAD_SHAPE;
-    const int num_sms = current_sms();
-    const bool direct = kv4_direct(B, Hkv, Nq, group, Nk, num_sms);
-    if (direct && (rows_q * H > (int64_t{1} << 31) - 1 ||           // its key tiles are counted in 32 bits
-                   static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(static_cast<int64_t>(Nq) * group) >
-                       (int64_t{1} << 31) - 1))
-        return FA_ERR_BAD_SHAPE;
     if (rows_q > 0 && (!q || !o || !lse)) return FA_ERR_NULLPTR;
     if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
     if (misaligned(q) || misaligned(k_codes) || misaligned(k_words) || misaligned(v_codes) ||
@@ -944,8 +953,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     if (rc != FA_OK) return rc;
     float* part = static_cast<float*>(workspace);
 
-    if (!direct) {
-        if (group > 65535) return FA_ERR_BAD_SHAPE;
+    if (!kv4_direct(B, Hkv, Nq, group, Nk, num_sms)) {
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
         const int ns = num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, st->num_sms);

@@ -82,6 +82,11 @@ def test_sizes():
     assert size(2, 8, 2, 1, 512, 128, 0, 0) >= 0 and size(2, 8, 2, 500, 512, 128, 0, 0) >= back
     assert size(2, 8, 3, 1, 512, 128, 0, 4) == 0       # 8 heads over 3: refused
     assert size(0, 8, 2, 1, 512, 128, 0, 4) == 0 and size(2, 8, 2, 1, 512, 128, 0, -1) == 0
+    # shapes that the call refuses, products of sizes past 64 bits among them
+    big = 2 ** 30
+    assert size(big, big, big, 256, 1024, 64, 0, 0) == 0 and size(1, big, 1, big, 1024, 64, 0, 0) == 0
+    assert size(2, 8, 2, 1, 508, 128, 0, 4) == 0 and size(2, 8, 2, 1, 512, 96, 0, 4) == 0
+    assert fa.fa_fwd_kv4(**attend_args(B=big, H=big, Hkv=big, Nq=256)) == -3
 
 
 # ------------------------------------------------------------- the binding --

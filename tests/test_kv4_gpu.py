@@ -453,6 +453,19 @@ def test_a_nan_row_reaches_only_the_queries_that_see_it(Nq, Hkv, which, num_spli
     assert torch.equal(o[0, ~sees], clean[0, ~sees]) and torch.equal(o[0, :, others], clean[0, :, others])
 
 
+@pytest.mark.parametrize("Nq,H,Hkv", [(1, 4, 2), (70, 4, 2), (250, 40, 20)])
+@pytest.mark.parametrize("num_splits", [0, 2])
+def test_a_window_as_wide_as_the_cache_is_none(Nq, H, Hkv, num_splits):
+    # also for queries that stand before the first key
+    cache = random_cache(2, 304, Hkv, 128, seed=18)
+    q = queries(2, Nq, H, 128, 6)
+    lens = torch.tensor([304, 30], dtype=torch.int32, device=DEV)
+    want, wlse = fa.forward_kv4(q, cache, lens, causal=True, num_splits=num_splits)
+    for window in (304, 305, 2 ** 31 - 1):
+        o, lse = fa.forward_kv4(q, cache, lens, causal=True, window=window, num_splits=num_splits)
+        assert torch.equal(o, want) and torch.equal(lse, wlse)
+
+
 def test_nan_queries_stay_alone():
     cache = random_cache(1, 256, 1, 64, seed=12)
     q = queries(1, 2, 8, 64, 5)
