@@ -458,7 +458,8 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
 }
 
 // ------------------------------------------------------ 4-bit K/V cache --
-// Query rows a CTA of kv4_decode_kernel holds: 8 or 16.
+// Query rows that a warp of the codes' kernels holds, 8 or 16, where it has
+// enough to do (kv4_plan), and the blocks of so many.
 int kv4_block_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
 int64_t kv4_row_blocks(int64_t rows) {
@@ -479,7 +480,7 @@ int64_t kv4_row_blocks(int64_t rows) {
 // items all run at once the limit grows by that.  There, d 128: B 2, 4 kv heads,
 // 4096 rows: group 1 and 200 queries 25 / 32, 512 queries 47 / 35; group 4 and
 // 50 queries 25 / 29, 100 queries 36 / 31; B 1, 8 kv heads, 2000 rows, group 1:
-// 100 queries 15 / 30, 512 queries 37 / 34.  Where not all run at once, B 4, 8 kv
+// 100 queries 13 / 30, 512 queries 37 / 34.  Where not all run at once, B 4, 8 kv
 // heads, 1024 rows, group 1 and 200 queries 36 / 28.
 bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int num_sms) {
     using C = fa::Kv4DecCfg<128, 2>;
@@ -502,23 +503,33 @@ bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int num_sms) {
 // of 8 kv heads: B 4, 1024 rows 7.1 / 9.9, 8192 rows (4 tiles) 13.1 / 15.9,
 // 16384 rows (8 tiles) 19.7 / 20.7, there with lengths from 0 up 17.8 / 16.8;
 // B 40, 1024 rows (4 tiles) 14.2 / 16.9, 4096 rows (16 tiles) 42.5 / 37.5.
+// Blocks of 8 rows are taken for more than 8 too where a cluster each fits: twice
+// the warps on what a block of 16 would do in one, at 3 CTAs an SM instead of 2.
+// Measured (us, 8 / 16), d 128, 8 kv heads: 16 rows, B 1, 2000 cache rows 10.0 /
+// 11.5, B 8, 1024 cache rows 10.1 / 12.6; 64 rows, B 1, 2000 cache rows 10.9 /
+// 14.1.  Where they do not fit, 64 rows, B 8, 1024 cache rows 26.0 / 16.6; 16
+// rows, B 16, 8192 cache rows 45.8 / 41.0.
 struct Kv4Plan {
-    int cluster, ranges;
+    int block_rows, cluster, ranges;
 };
 
 Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_splits, int num_sms) {
     using C1 = fa::Kv4DecCfg<128, 1>;
     using C2 = fa::Kv4DecCfg<128, 2>;
-    const int64_t rows = static_cast<int64_t>(Nq) * group;
-    const int64_t items = static_cast<int64_t>(B) * Hkv * kv4_row_blocks(rows);
-    if (num_splits > 0) return {0, static_cast<int>(std::min<int64_t>(items * num_splits, 1 << 20))};
-    const int ctas = num_sms * (kv4_block_rows(rows) == 8 ? C1::MIN_CTAS : C2::MIN_CTAS);
+    const int64_t rows = static_cast<int64_t>(Nq) * group, heads = static_cast<int64_t>(B) * Hkv;
+    const int most = kv4_block_rows(rows);
+    if (num_splits > 0)
+        return {most, 0, static_cast<int>(std::min<int64_t>(heads * kv4_row_blocks(rows) * num_splits, 1 << 20))};
     const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq + C1::BN) : Nk;
     const int64_t tiles = (keys + C1::BN - 1) / C1::BN;
-    int cluster = 8;
-    while (cluster > 1 && (items * cluster > ctas || tiles <= C1::WARPS * cluster / 2)) cluster /= 2;
-    if (items * cluster <= ctas && tiles <= 6 * C1::WARPS * cluster) return {cluster, 0};
-    return {0, ctas * C1::WARPS};
+    for (int per = 8; per <= most; per += 8) {
+        const int64_t items = heads * ((rows + per - 1) / per);
+        const int ctas = num_sms * (per == 8 ? C1::MIN_CTAS : C2::MIN_CTAS);
+        int cluster = 8;
+        while (cluster > 1 && (items * cluster > ctas || tiles <= C1::WARPS * cluster / 2)) cluster /= 2;
+        if (items * cluster <= ctas && tiles <= 6 * C1::WARPS * cluster) return {per, cluster, 0};
+    }
+    return {most, 0, num_sms * (most == 8 ? C1::MIN_CTAS : C2::MIN_CTAS) * C1::WARPS};
 }
 
 int current_sms() {
@@ -540,8 +551,8 @@ size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, 
     const int group = H / Hkv;
     if (!kv4_direct(B, Hkv, Nq, group, Nk, num_sms))
         return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
-    const size_t rows = 2 * static_cast<size_t>(kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms).ranges) *
-                        kv4_block_rows(static_cast<int64_t>(Nq) * group);
+    const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms);
+    const size_t rows = 2 * static_cast<size_t>(plan.ranges) * plan.block_rows;
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
 
@@ -1000,19 +1011,18 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     p.Nk = Nk;
     p.causal = causal ? 1 : 0;
     p.window = window > 0 ? window : 0;
-    const int64_t rows = static_cast<int64_t>(Nq) * group;
-    p.row_blocks = static_cast<int>(kv4_row_blocks(rows));
-    const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, st->num_sms);
+    const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms);
+    p.row_blocks = static_cast<int>((static_cast<int64_t>(Nq) * group + plan.block_rows - 1) / plan.block_rows);
     p.ranges = plan.ranges;
     p.o_part = part;
-    p.ml_part = reinterpret_cast<float2*>(part + 2 * static_cast<size_t>(p.ranges) * kv4_block_rows(rows) * d);
+    p.ml_part = reinterpret_cast<float2*>(part + 2 * static_cast<size_t>(p.ranges) * plan.block_rows * d);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.error_word = st->error_word;
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
     p.fault_skip = g_fault_mode == 3 ? 1 : 0;
     if (d == 64)
-        return kv4_block_rows(rows) == 8 ? launch_kv4_decode<64, 1>(p, plan, stream) : launch_kv4_decode<64, 2>(p, plan, stream);
-    return kv4_block_rows(rows) == 8 ? launch_kv4_decode<128, 1>(p, plan, stream) : launch_kv4_decode<128, 2>(p, plan, stream);
+        return plan.block_rows == 8 ? launch_kv4_decode<64, 1>(p, plan, stream) : launch_kv4_decode<64, 2>(p, plan, stream);
+    return plan.block_rows == 8 ? launch_kv4_decode<128, 1>(p, plan, stream) : launch_kv4_decode<128, 2>(p, plan, stream);
 }
 
 size_t fa_fp8_vt_bytes(int B, int H, int N, int d) {
