@@ -89,16 +89,37 @@ __device__ __forceinline__ uint32_t bf2_min_nan(uint32_t a, uint32_t b) {
     return r;
 }
 
-// {low: max x, high: -min x} of a row that LANES neighbouring lanes hold, 8
-// channels (one bf16 pair a word) each; NaN where x has one.
-template <int LANES>
-__device__ __forceinline__ uint32_t kv4_reduce(const uint4& x) {
+// {low: max x, high: -min x} of 8 channels (one bf16 pair a word); NaN where x has one.
+__device__ __forceinline__ uint32_t kv4_extremes(const uint4& x) {
     const uint32_t up = bf2_max_nan(bf2_max_nan(x.x, x.y), bf2_max_nan(x.z, x.w));
     const uint32_t dn = bf2_min_nan(bf2_min_nan(x.x, x.y), bf2_min_nan(x.z, x.w)) ^ 0x80008000u;
-    uint32_t m = bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+    return bf2_max_nan(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+}
+
+// The same of whole rows, each held by LANES neighbouring lanes, a row of each
+// of ITER steps: lane c of a group returns those of step c % ITER.  The lanes
+// halve the steps they hold with each exchange (ITER - 1 of them, not
+// log2(LANES) for every step).
+template <int LANES, int ITER>
+__device__ __forceinline__ uint32_t kv4_row_extremes(const uint4 (&x)[ITER]) {
+    uint32_t m[ITER];
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = bf2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+    for (int it = 0; it < ITER; ++it) m[it] = kv4_extremes(x[it]);
+    const int lane = lane_id();
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+        if (o < ITER) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < ITER / 2 / o; ++i) {
+                const uint32_t keep = upper ? m[2 * i + 1] : m[2 * i], send = upper ? m[2 * i] : m[2 * i + 1];
+                m[i] = bf2_max_nan(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            }
+        } else {
+            m[0] = bf2_max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        }
+    }
+    return m[0];
 }
 
 // How a row is rounded: x * inv + base cut to an integer is 128 + c.
@@ -138,22 +159,18 @@ __device__ __forceinline__ Kv4Scale kv4_scale(uint32_t m) {
 // from where byte permutes collect it.
 __device__ __forceinline__ uint32_t kv4_encode(const uint4& x, float inv, float base, bool clamp) {
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    float e[4], o[4];
+    float2 c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        e[j] = fmaf(__uint_as_float(xs[j] << 16), inv, base);
-        o[j] = fmaf(__uint_as_float(xs[j] & 0xffff0000u), inv, base);
-    }
+    for (int j = 0; j < 4; ++j)
+        c[j] = ffma2(make_float2(__uint_as_float(xs[j] << 16), __uint_as_float(xs[j] & 0xffff0000u)),
+                     make_float2(inv, inv), make_float2(base, base));
     if (clamp) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            e[j] = fminf(e[j], 143.9f);
-            o[j] = fminf(o[j], 143.9f);
-        }
+        for (int j = 0; j < 4; ++j) c[j] = make_float2(fminf(c[j].x, 143.9f), fminf(c[j].y, 143.9f));
     }
     auto third = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0062); };
-    const uint32_t even = __byte_perm(third(e[0], e[1]), third(e[2], e[3]), 0x5410);
-    const uint32_t odd = __byte_perm(third(o[0], o[1]), third(o[2], o[3]), 0x5410);
+    const uint32_t even = __byte_perm(third(c[0].x, c[1].x), third(c[2].x, c[3].x), 0x5410);
+    const uint32_t odd = __byte_perm(third(c[0].y, c[1].y), third(c[2].y, c[3].y), 0x5410);
     return even + odd * 16u;
 }
 
@@ -190,62 +207,66 @@ constexpr int kKv4Warps = 8;
 template <int D, int ITER>
 __host__ __device__ constexpr int kv4_tokens() { return ITER * (32 / (D / 8)); }
 
-// Rows of the cache arrays of a warp's tokens and head h: lane j holds token
-// j's (below 0: not taken).
+// What a warp works on: tokens first .. first + TOK - 1 of head h.
+struct Kv4Unit {
+    int64_t first;
+    int h, left;        // left: how many of the tokens exist
+};
+
 template <int TOK>
-__device__ __forceinline__ int64_t kv4_warp_rows(const Kv4Params& p, int64_t first, int h) {
+__device__ __forceinline__ Kv4Unit kv4_unit(const Kv4Params& p) {
+    const uint32_t unit = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);    // the host keeps units below 2^31
+    const uint32_t chunk = unit / static_cast<uint32_t>(p.place.H);
+    const int64_t first = static_cast<int64_t>(chunk) * TOK;
+    const int64_t left = p.rows - first;
+    return {first, static_cast<int>(unit - chunk * p.place.H), static_cast<int>(left < TOK ? left : TOK)};
+}
+
+// Row of the cache arrays of a unit's token; below 0 where it is not taken.
+__device__ __forceinline__ int64_t kv4_row(const Kv4Params& p, const Kv4Unit& u, int token) {
     int b, pos;
-    if (lane_id() >= TOK || !kv4_place(p.place, first + lane_id(), p.rows, b, pos)) return -1;
-    return (static_cast<int64_t>(b) * p.place.H + h) * p.place.Nk + pos;
+    if (token >= u.left || !kv4_place(p.place, u.first + token, p.rows, b, pos)) return -1;
+    return (static_cast<int64_t>(b) * p.place.H + u.h) * p.place.Nk + pos;
 }
 
 // Writes bf16 rows into the cache.  blockIdx.y selects K or V.
 //
 // Instructions bound it as soon as there are many a value (the integer pipe
-// does half of them): a row's scale is found by one lane, lane j for token j,
-// once its maxima are there, not by all that hold the row.  At 1.39 GB read
-// and written: 221 us with the library's correctly rounded division and
-// reciprocal by every lane, 155 us with approximations that are exact here,
-// 126 us with a lane to a token.
+// does half of them): a row's scale is found by one lane, not by all that hold
+// the row, and the row's extremes come to that lane by exchanges that halve
+// what a lane holds.  At 0.69 GB read and written (106 us at the copy rate):
+// 221 us with the library's correctly rounded division and reciprocal by every
+// lane, 155 us with approximations that are exact here, 126 us with a lane to a
+// token, 112 us with the halving exchanges, packed products and addresses that
+// advance by a step.
 template <int D, int ITER>
 __global__ void __launch_bounds__(kKv4Warps * 32)
 kv4_write_kernel(const Kv4Params p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, TOK = kv4_tokens<D, ITER>();
-    const int lane = lane_id();
-    const int H = p.place.H;
-    const uint32_t unit = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);    // the host keeps units below 2^31
-    const uint32_t chunk = unit / static_cast<uint32_t>(H);
-    const int h = static_cast<int>(unit - chunk * H);
-    const int64_t first = static_cast<int64_t>(chunk) * TOK;
-    if (first >= p.rows) return;
-    const __nv_bfloat16* x = blockIdx.y ? p.x[1] : p.x[0];
-    uint8_t* codes = blockIdx.y ? p.codes[1] : p.codes[0];
-    uint16_t* words = blockIdx.y ? p.words[1] : p.words[0];
-    const int sub = lane / LANES, c8 = lane % LANES;
+    const Kv4Unit u = kv4_unit<TOK>(p);
+    if (u.left <= 0) return;
+    const int lane = lane_id(), sub = lane / LANES, c8 = lane % LANES;
+    const __nv_bfloat16* x = (blockIdx.y ? p.x[1] : p.x[0]) + ((u.first + sub) * p.place.H + u.h) * D + c8 * 8;
+    const int64_t step = static_cast<int64_t>(ROWS) * p.place.H * D;
     uint4 v[ITER];
 #pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-        const int64_t r = first + it * ROWS + sub;
-        v[it] = r < p.rows ? __ldcs(reinterpret_cast<const uint4*>(x + (r * H + h) * D + c8 * 8))
-                           : make_uint4(0, 0, 0, 0);
-    }
-    const int64_t row = kv4_warp_rows<TOK>(p, first, h);
-    uint32_t mine = 0;              // the maxima of token `lane`
-#pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-        const uint32_t m = __shfl_sync(0xffffffffu, kv4_reduce<LANES>(v[it]), lane % ROWS * LANES);
-        if (lane / ROWS == it) mine = m;
-    }
-    const Kv4Scale s = kv4_scale(mine);
+    for (int it = 0; it < ITER; ++it)
+        v[it] = it * ROWS + sub < u.left ? __ldcs(reinterpret_cast<const uint4*>(x + it * step))
+                                         : make_uint4(0, 0, 0, 0);
+    const int64_t row = kv4_row(p, u, c8 % ITER * ROWS + sub);
+    const Kv4Scale s = kv4_scale(kv4_row_extremes<LANES, ITER>(v));
     const bool clamp = __any_sync(0xffffffffu, s.clamp);
-    if (row >= 0) words[row] = static_cast<uint16_t>(s.word);
+    if (row >= 0 && c8 < ITER) (blockIdx.y ? p.words[1] : p.words[0])[row] = static_cast<uint16_t>(s.word);
+    uint8_t* codes = (blockIdx.y ? p.codes[1] : p.codes[0]) + c8 * 4;
+    const int64_t mine = row * (D / 2);
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-        const float inv = __shfl_sync(0xffffffffu, s.inv, it * ROWS + sub);
-        const float base = __shfl_sync(0xffffffffu, s.base, it * ROWS + sub);
-        const int64_t to = __shfl_sync(0xffffffffu, row, it * ROWS + sub);
+        const int from = sub * LANES + it;
+        const float inv = __shfl_sync(0xffffffffu, s.inv, from);
+        const float base = __shfl_sync(0xffffffffu, s.base, from);
+        const int64_t to = __shfl_sync(0xffffffffu, mine, from);
         const uint32_t c = kv4_encode(v[it], inv, base, clamp);
-        if (to >= 0) *reinterpret_cast<uint32_t*>(codes + to * (D / 2) + c8 * 4) = c;
+        if (to >= 0) *reinterpret_cast<uint32_t*>(codes + to) = c;
     }
 }
 
@@ -256,41 +277,34 @@ template <int D, int ITER>
 __global__ void __launch_bounds__(kKv4Warps * 32)
 kv4_read_kernel(const Kv4Params p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, TOK = kv4_tokens<D, ITER>();
-    const int lane = lane_id();
-    const int H = p.place.H;
-    const uint32_t unit = blockIdx.x * kKv4Warps + (threadIdx.x >> 5);    // the host keeps units below 2^31
-    const uint32_t chunk = unit / static_cast<uint32_t>(H);
-    const int h = static_cast<int>(unit - chunk * H);
-    const int64_t first = static_cast<int64_t>(chunk) * TOK;
-    if (first >= p.rows) return;
-    const uint8_t* codes = blockIdx.y ? p.codes[1] : p.codes[0];
+    const Kv4Unit u = kv4_unit<TOK>(p);
+    if (u.left <= 0) return;
+    const int lane = lane_id(), sub = lane / LANES, c8 = lane % LANES;
+    const uint8_t* codes = (blockIdx.y ? p.codes[1] : p.codes[0]) + c8 * 4;
     const uint16_t* words = blockIdx.y ? p.words[1] : p.words[0];
     const uint16_t* other = blockIdx.y ? p.words[0] : p.words[1];
-    __nv_bfloat16* x = blockIdx.y ? p.x[1] : p.x[0];
-    const int sub = lane / LANES, c8 = lane % LANES;
-    const int64_t from = kv4_warp_rows<TOK>(p, first, h);
-    uint32_t c[ITER], word[ITER];
+    // a token a lane: its row, and the row's word
+    const int64_t row = lane < TOK ? kv4_row(p, u, lane) : -1;
+    const int64_t mine = row * (D / 2);
+    uint32_t c[ITER];
     bool taken[ITER];
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-        const int64_t row = __shfl_sync(0xffffffffu, from, it * ROWS + sub);
-        taken[it] = row >= 0;
-        c[it] = word[it] = 0;
-        if (taken[it]) {
-            c[it] = *reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + c8 * 4);
-            word[it] = words[row];
-            if (p.poison) {
-                const bool nan = word[it] >= 0x7f80u || other[row] >= 0x7f80u;
-                if (nan) word[it] = blockIdx.y == 0 ? kKv4NaN : 0u;
-            }
-        }
+        const int64_t from = __shfl_sync(0xffffffffu, mine, it * ROWS + sub);
+        taken[it] = from >= 0;
+        c[it] = taken[it] ? *reinterpret_cast<const uint32_t*>(codes + from) : 0u;
     }
+    uint32_t word = 0;
+    if (row >= 0) {
+        word = words[row];
+        if (p.poison && (word >= 0x7f80u || other[row] >= 0x7f80u)) word = blockIdx.y == 0 ? kKv4NaN : 0u;
+    }
+    __nv_bfloat16* x = (blockIdx.y ? p.x[1] : p.x[0]) + ((u.first + sub) * p.place.H + u.h) * D + c8 * 8;
+    const int64_t step = static_cast<int64_t>(ROWS) * p.place.H * D;
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-        if (taken[it]) {
-            const int64_t r = first + it * ROWS + sub;
-            *reinterpret_cast<uint4*>(x + (r * H + h) * D + c8 * 8) = kv4_decode(c[it], word[it]);
-        }
+        const uint32_t w = __shfl_sync(0xffffffffu, word, it * ROWS + sub);
+        if (taken[it]) *reinterpret_cast<uint4*>(x + it * step) = kv4_decode(c[it], w);
     }
 }
 
