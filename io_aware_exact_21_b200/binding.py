@@ -492,7 +492,7 @@ def _kv4_cache_fits(torch, kc, kw, vc, vw, index):
             and kw.shape == words and vw.shape == words
             and kc.is_contiguous() and vc.is_contiguous() and kw.is_contiguous() and vw.is_contiguous()
             and kc.get_device() == vc.get_device() == kw.get_device() == vw.get_device() == index
-            and index == torch._C._cuda_getDevice())
+            and index == torch.cuda.current_device())
 
 
 def _int32_fits(torch, t, n, index):
