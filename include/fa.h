@@ -229,7 +229,7 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * it, and reaches no others.  Elements of q are below 2^116 in magnitude (or
  * O of their query is unspecified).
  *   Few query rows to a key/value head (Nq * H / Hkv; up to 96 with a head
- * each, 192 with four to a head, more where the whole problem is small) run on
+ * each, 240 with four to a head, more where the whole problem is small) run on
  * kernels that multiply the 4-bit codes as they are; more are run by reading
  * the rows in use back into the workspace for the tensor-core forward.
  *   num_splits : few rows: the keys of all sequences and heads together are

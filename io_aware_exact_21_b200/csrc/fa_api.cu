@@ -467,31 +467,11 @@ int64_t kv4_row_blocks(int64_t rows) {
     return (rows + per - 1) / per;
 }
 
-// Whether attention over the 4-bit cache multiplies the codes as they are, 16
-// query rows to a warp, or reads the rows back for the forward, whose blocks
-// hold 256 queries of one head.  The one's time goes with the rows, Nq * group;
-// the other's with the blocks of the group's heads, whatever they hold, and
-// with the rows read back.  Measured (us, codes / read back), B 16, 8 kv heads,
-// 8192 rows, d 128: group 1 and 64 queries 120 / 257; group 4 and 32 queries
-// 226 / 525, 64 queries 429 / 527; B 32, 2 kv heads, 1000 rows, d 64, group 4:
-// 16 queries 14 / 44, 64 queries 54 / 44.
-// The read-back's three launches cost 20 us or so besides, in which the codes'
-// kernel does 32 passes of 16 rows over a tile of 64 keys on each SM; while its
-// items all run at once the limit grows by that.  There, d 128: B 2, 4 kv heads,
-// 4096 rows: group 1 and 200 queries 25 / 32, 512 queries 47 / 35; group 4 and
-// 50 queries 25 / 29, 100 queries 36 / 31; B 1, 8 kv heads, 2000 rows, group 1:
-// 100 queries 13 / 30, 512 queries 37 / 34.  Where not all run at once, B 4, 8 kv
-// heads, 1024 rows, group 1 and 200 queries 36 / 28.
-bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int num_sms) {
-    using C = fa::Kv4DecCfg<128, 2>;
-    const int64_t rows = static_cast<int64_t>(Nq) * group;
-    int64_t limit = 64 + 32 * static_cast<int64_t>(group) * ((Nq + 255) / 256);
-    const int64_t heads = static_cast<int64_t>(B) * Hkv;
-    if (rows <= limit || Nk == 0 || heads == 0) return true;
-    const int64_t slots = static_cast<int64_t>(num_sms) * C::MIN_CTAS;
-    if (heads <= slots && heads * kv4_row_blocks(rows) <= slots)
-        limit += static_cast<int64_t>(num_sms) * 32 * 16 / (heads * ((Nk + C::BN - 1) / C::BN));
-    return rows <= limit;
+// Key tiles that a sequence has at most.
+int64_t kv4_tiles(int Nq, int Nk, int window) {
+    constexpr int BN = fa::Kv4DecCfg<128, 1>::BN;
+    const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq + BN) : Nk;
+    return (keys + BN - 1) / BN;
 }
 
 // How the key tiles are dealt out: to a cluster of `cluster` CTAs each item
@@ -520,8 +500,7 @@ Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_
     const int most = kv4_block_rows(rows);
     if (num_splits > 0)
         return {most, 0, static_cast<int>(std::min<int64_t>(heads * kv4_row_blocks(rows) * num_splits, 1 << 20))};
-    const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq + C1::BN) : Nk;
-    const int64_t tiles = (keys + C1::BN - 1) / C1::BN;
+    const int64_t tiles = kv4_tiles(Nq, Nk, window);
     for (int per = 8; per <= most; per += 8) {
         const int64_t items = heads * ((rows + per - 1) / per);
         const int ctas = num_sms * (per == 8 ? C1::MIN_CTAS : C2::MIN_CTAS);
@@ -530,6 +509,26 @@ Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_
         if (items * cluster <= ctas && tiles <= 6 * C1::WARPS * cluster) return {per, cluster, 0};
     }
     return {most, 0, num_sms * (most == 8 ? C1::MIN_CTAS : C2::MIN_CTAS) * C1::WARPS};
+}
+
+// Whether attention over the 4-bit cache multiplies the codes as they are, or
+// reads the rows back for the forward, whose blocks hold 256 queries of one head.
+// A problem that clusters take is short enough for the codes in any case: the
+// read-back's three launches alone cost as much.  Beyond that the codes' time
+// goes with the rows, Nq * group, and the read-back's with the blocks of the
+// group's heads, whatever they hold, and with the rows read back; with few tiles
+// the merge of many short items weighs on the codes.  Measured (us, codes / read
+// back), 8 kv heads, d 128.  Clusters: B 1, 512 cache rows, 512 queries 13 / 18,
+// group 4 and 100 queries 11 / 17; B 1, 2000 rows, group 4 and 70 queries 19 / 23.
+// B 16, 4096 rows: group 1 and 64 queries 75 / 106, 100 queries 119 / 106; group 4
+// and 50 queries 205 / 246, 70 queries 277 / 246; group 8 and 40 queries 308 / 403,
+// 64 queries 479 / 406.  Few tiles, B 4, 1024 rows: group 4 and 50 queries 35 /
+// 26, group 1 and 150 queries 31 / 24.
+bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int window, int num_sms) {
+    const int64_t rows = static_cast<int64_t>(Nq) * group;
+    const int64_t blocks = static_cast<int64_t>(group) * ((Nq + 255) / 256);
+    return Nk == 0 || rows <= (kv4_tiles(Nq, Nk, window) >= 32 ? 48 : 36) * (1 + blocks) ||
+           kv4_plan(B, Hkv, Nq, group, Nk, window, 0, num_sms).cluster > 0;
 }
 
 int current_sms() {
@@ -545,12 +544,28 @@ size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
     return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
+// Ranges that a chunk's keys are cut into: as many as the SMs hold blocks of 256
+// queries at once, never more (a second round of blocks costs as much as the
+// first), of 4 key tiles of 128 at least, and one below 16 tiles (B 4, 8 heads,
+// 1024 rows, 512 queries: 28 for one, 32 for two).  Measured (us, for 1, 2, 4, 5, 8
+// ranges), 8 kv heads, 16384 rows, d 128: group 4 and 100 queries (32 blocks)
+// 240, 134, 81, 121, 87; 512 queries (64 blocks) 244, 147, 156, 190, 177; group 1
+// and 512 queries (16 blocks) 241, 138, 85, 76, 61, and 85 for 10; B 2, 16 heads,
+// 4096 rows, 1000 queries (128 blocks) 79, 98, 116, 131, 147.
+int kv4_chunk_splits(int B, int H, int Nq, int Nk, int window, int num_sms) {
+    const int64_t items = static_cast<int64_t>(B) * H * ((Nq + 255) / 256);
+    const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq) : Nk;
+    const int64_t tiles = (keys + 127) / 128;
+    const int64_t most = tiles < 16 ? 1 : std::min<int64_t>(fa::kDecMaxSplits, tiles / 4);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / std::max<int64_t>(items, 1), most)));
+}
+
 // Bytes of the partial results: of the ranges (two of ROWS rows, each with its
 // maximum and sum), or of a chunk's splits.
 size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const int group = H / Hkv;
-    if (!kv4_direct(B, Hkv, Nq, group, Nk, num_sms))
-        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, num_sms));
+    if (!kv4_direct(B, Hkv, Nq, group, Nk, window, num_sms))
+        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Nq, Nk, window, num_sms));
     const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms);
     const size_t rows = 2 * static_cast<size_t>(plan.ranges) * plan.block_rows;
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
@@ -558,7 +573,7 @@ size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, 
 
 size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
-    return kv4_direct(B, Hkv, Nq, H / Hkv, Nk, num_sms) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
+    return kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
 }
 
 bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
@@ -568,13 +583,13 @@ bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
 }
 
 // Shapes that fa_fwd_kv4 refuses.
-bool kv4_bad_attention(int B, int H, int Hkv, int Nq, int Nk, int d, int num_sms) {
+bool kv4_bad_attention(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_sms) {
     constexpr int64_t kMax = (int64_t{1} << 31) - 1;
     if (H <= 0 || Nq < 0 || kv4_bad_cache(B, Hkv, Nk, d) || H % Hkv != 0) return true;
     const int64_t rows_q = static_cast<int64_t>(B) * Nq, rows = static_cast<int64_t>(Nq) * (H / Hkv);
     if (rows_q > kMax || rows_q * H > (int64_t{1} << 40) / d || rows > kMax) return true;
     if (rows_q == 0) return false;
-    if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, num_sms)) return H / Hkv > 65535;
+    if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms)) return H / Hkv > 65535;
     return rows_q * H > kMax ||      // a CTA each in the merge; the key tiles are counted in 32 bits
            static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(rows) > kMax;
 }
@@ -930,7 +945,7 @@ int fa_dequantize_kv4(const void* k_codes, const void* k_words, const void* v_co
 size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits) {
     const int num_sms = current_sms();
     if ((d != 64 && d != 128) || num_splits < 0 || num_splits > fa::kDecMaxSplits ||
-        kv4_bad_attention(B, H, Hkv, Nq, Nk, d, num_sms) || B == 0 || Nq == 0)
+        kv4_bad_attention(B, H, Hkv, Nq, Nk, d, window, num_sms) || B == 0 || Nq == 0)
         return 0;
     return kv4_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
 }
@@ -941,7 +956,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
     const int num_sms = current_sms();
-    if (kv4_bad_attention(B, H, Hkv, Nq, Nk, d, num_sms)) return FA_ERR_BAD_SHAPE;
+    if (kv4_bad_attention(B, H, Hkv, Nq, Nk, d, window, num_sms)) return FA_ERR_BAD_SHAPE;
     if (num_splits < 0 || num_splits > fa::kDecMaxSplits) return FA_ERR_BAD_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_BAD_SCALE;
     if (window > 0 && !causal) return FA_ERR_BAD_MASK;
@@ -964,10 +979,10 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     if (rc != FA_OK) return rc;
     float* part = static_cast<float*>(workspace);
 
-    if (!kv4_direct(B, Hkv, Nq, group, Nk, num_sms)) {
+    if (!kv4_direct(B, Hkv, Nq, group, Nk, window, num_sms)) {
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
-        const int ns = num_splits > 0 ? num_splits : prefill_splits(B, H, Nq, Nk, st->num_sms);
+        const int ns = num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Nq, Nk, window, num_sms);
         uint8_t* back = static_cast<uint8_t*>(workspace) + decode_workspace_bytes(B, H, Nq, d, ns);
         void* kb = back;
         void* vb = back + kv4_readback_bytes(B, Hkv, Nk, d);
