@@ -445,16 +445,8 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
                            : launch_fwd_cache<128>(mq, mk, mv, p, grid, stream);
     prof_stop(0, slot, stream);
     if (rc != FA_OK || ns == 1) return rc;
-    const int64_t warps = rows_q * H;
-    const int slot2 = prof_start(5, stream);
-    if (d == 64)
-        fa::combine_kernel<64><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
-            p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
-    else
-        fa::combine_kernel<128><<<static_cast<int>((warps + 7) / 8), 256, 0, stream>>>(
-            p.kv.o_part, p.kv.lse_part, p.o, lse, static_cast<int>(rows_q), H, Nq, ns);
-    prof_stop(5, slot2, stream);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return d == 64 ? launch_combine<64>(p.kv.o_part, p.kv.lse_part, p.o, lse, B, H, Nq, ns, stream)
+                   : launch_combine<128>(p.kv.o_part, p.kv.lse_part, p.o, lse, B, H, Nq, ns, stream);
 }
 
 // ------------------------------------------------------ 4-bit K/V cache --
