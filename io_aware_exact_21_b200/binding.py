@@ -479,25 +479,30 @@ def _expect_kv4_cache(cache, B, Hkv, d, device):
 
 # The calls of a decode step are short, and their checks are a good part of the
 # time: what fits is seen in one look (below), and only what does not goes
-# through the _expect functions, which say why.
+# through the _expect functions, which say why; the library is called with the
+# pointers, not through the functions above that look each argument over.
 
 def _kv4_cache_fits(torch, kc, kw, vc, vw, index):
-    """Whether these are a 4-bit cache's arrays on the current CUDA device `index`."""
+    """The shape of the codes where these are a 4-bit cache's arrays on the
+    current CUDA device `index`, else None."""
     if kc is None or kw is None or vc is None or vw is None:
-        return False
+        return None
     codes = kc.shape
-    words = codes[:3]
-    return (len(codes) == 4 and kc.dtype is torch.uint8 and vc.dtype is torch.uint8
+    if len(codes) != 4:
+        return None
+    words = (codes[0], codes[1], codes[2])
+    if (kc.dtype is torch.uint8 and vc.dtype is torch.uint8
             and kw.dtype is torch.int16 and vw.dtype is torch.int16 and vc.shape == codes
             and kw.shape == words and vw.shape == words
             and kc.is_contiguous() and vc.is_contiguous() and kw.is_contiguous() and vw.is_contiguous()
             and kc.get_device() == vc.get_device() == kw.get_device() == vw.get_device() == index
-            and index == torch.cuda.current_device())
+            and index == torch.cuda.current_device()):
+        return codes
+    return None
 
 
 def _int32_fits(torch, t, n, index):
-    return (t.dtype is torch.int32 and t.get_device() == index and t.dim() == 1 and t.shape[0] == n
-            and t.is_contiguous())
+    return t.dtype is torch.int32 and t.get_device() == index and t.shape == (n,) and t.is_contiguous()
 
 
 def _kv4_rows(k, v, cache, cu_seqlens, starts, lens):
@@ -507,14 +512,15 @@ def _kv4_rows(k, v, cache, cu_seqlens, starts, lens):
     kc, kw, vc, vw = (cache.get("k_codes"), cache.get("k_words"), cache.get("v_codes"),
                       cache.get("v_words"))
     index = -1 if k is None else k.get_device()
-    if index >= 0 and v is not None and _kv4_cache_fits(torch, kc, kw, vc, vw, index):
-        B, Hkv, Nk, half = kc.shape
+    codes = _kv4_cache_fits(torch, kc, kw, vc, vw, index) if index >= 0 and v is not None else None
+    if codes is not None:
+        B, Hkv, Nk, half = codes
         shape = k.shape
         if (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and v.shape == shape
                 and v.get_device() == index and k.is_contiguous() and v.is_contiguous()
-                and shape[-2:] == (Hkv, 2 * half)
                 and (len(shape) == 4 and shape[0] == B if cu_seqlens is None else
                      len(shape) == 3 and lens is None and _int32_fits(torch, cu_seqlens, B + 1, index))
+                and shape[-2] == Hkv and shape[-1] == 2 * half
                 and (starts is None or _int32_fits(torch, starts, B, index))
                 and (lens is None or _int32_fits(torch, lens, B, index))):
             return kc, kw, vc, vw, B, shape[-3], Hkv, Nk, 2 * half
@@ -544,8 +550,9 @@ def quantize_kv4(k, v, cache, starts=None, lens=None, cu_seqlens=None, stream=No
     all); or packed [T, Hkv, d] with int32 ``cu_seqlens``.  Rows that fall
     outside the cache are left out.  Returns the cache."""
     kc, kw, vc, vw, B, N, Hkv, Nk, d = _kv4_rows(k, v, cache, cu_seqlens, starts, lens)
-    _check(fa_quantize_kv4(k, v, kc, kw, vc, vw, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
-           "fa_quantize_kv4")
+    _check(load_library().fa_quantize_kv4(
+        k.data_ptr(), v.data_ptr(), kc.data_ptr(), kw.data_ptr(), vc.data_ptr(), vw.data_ptr(), B, N,
+        Hkv, Nk, d, _ptr(cu_seqlens), _ptr(starts), _ptr(lens), _stream(stream)), "fa_quantize_kv4")
     return cache
 
 
@@ -570,8 +577,9 @@ def dequantize_kv4(cache, rows=None, starts=None, lens=None, cu_seqlens=None, ou
     kc, kw, vc, vw, B, N, Hkv, Nk, d = _kv4_rows(k, v, cache, cu_seqlens, starts, lens)
     if rows is not None and rows != N:
         raise ValueError("out holds %d rows, rows is %d" % (N, rows))
-    _check(fa_dequantize_kv4(kc, kw, vc, vw, k, v, B, N, Hkv, Nk, d, cu_seqlens, starts, lens, stream),
-           "fa_dequantize_kv4")
+    _check(load_library().fa_dequantize_kv4(
+        kc.data_ptr(), kw.data_ptr(), vc.data_ptr(), vw.data_ptr(), k.data_ptr(), v.data_ptr(), B, N,
+        Hkv, Nk, d, _ptr(cu_seqlens), _ptr(starts), _ptr(lens), _stream(stream)), "fa_dequantize_kv4")
     return k, v
 
 
@@ -586,7 +594,7 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
                       cache.get("v_words"))
     index = -1 if q is None else q.get_device()
     fits = index >= 0 and q.dim() == 4 and q.dtype is torch.bfloat16 and q.is_contiguous() \
-        and _kv4_cache_fits(torch, kc, kw, vc, vw, index) \
+        and _kv4_cache_fits(torch, kc, kw, vc, vw, index) is not None \
         and (seqlens_k is None or _int32_fits(torch, seqlens_k, q.shape[0], index))
     if not fits:
         _rank(q, "q", (4,))
@@ -611,14 +619,17 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
         lse = q.new_empty((B, H, Nq), dtype=torch.float32)
     else:
         _expect(lse, "lse", (B, H, Nq), torch.float32, q.device)
-    need = fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
+    lib = load_library()
+    window, num_splits = int(window), int(num_splits)
+    need = lib.fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits)
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, q.device)
     elif need:
         workspace = q.new_empty(need, dtype=torch.uint8)
-    _check(fa_fwd_kv4(q, kc, kw, vc, vw, out, lse, B, H, Hkv, Nq, Nk, d, scale, causal, window, seqlens_k,
-                      num_splits, workspace, 0 if workspace is None else workspace.numel(), stream),
-           "fa_fwd_kv4")
+    _check(lib.fa_fwd_kv4(
+        q.data_ptr(), kc.data_ptr(), kw.data_ptr(), vc.data_ptr(), vw.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), B, H, Hkv, Nq, Nk, d, float(scale), int(causal), window, _ptr(seqlens_k), num_splits,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)), "fa_fwd_kv4")
     return out, lse
 
 

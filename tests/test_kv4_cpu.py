@@ -94,9 +94,17 @@ def test_sizes():
 @pytest.fixture
 def calls(monkeypatch):
     rec = []
+    lib = fa.load_library()
+
+    class Library:
+        def __getattr__(self, name):
+            if name in ("fa_quantize_kv4", "fa_dequantize_kv4", "fa_fwd_kv4"):
+                return lambda *args: rec.append((name, args)) or 0
+            return getattr(lib, name)
+
     monkeypatch.setattr(bd, "_require_cuda", lambda t, name: None)
-    for name in ("fa_quantize_kv4", "fa_dequantize_kv4", "fa_fwd_kv4"):
-        monkeypatch.setattr(bd, name, lambda *a, _n=name: rec.append((_n, a)) or 0)
+    monkeypatch.setattr(bd, "load_library", Library)
+    monkeypatch.setattr(bd, "_stream", lambda stream: stream)
     return rec
 
 
