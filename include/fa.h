@@ -228,10 +228,10 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * stands for NaN makes O NaN (and LSE unspecified) for the queries that see
  * it, and reaches no others.  Elements of q are below 2^116 in magnitude (or
  * O of their query is unspecified).
- *   Few query rows to a key/value head (Nq * H / Hkv; up to 96 with a head
- * each, 240 with four to a head, more where the whole problem is small) run on
- * kernels that multiply the 4-bit codes as they are; more are run by reading
- * the rows in use back into the workspace for the tensor-core forward.
+ *   Few query rows to a key/value head (Nq * H / Hkv up to about 100, more where
+ * the whole problem is small) run on kernels that multiply the 4-bit codes as
+ * they are; more are run by reading the rows in use back into the workspace for
+ * the tensor-core forward.
  *   num_splits : few rows: the keys of all sequences and heads together are
  * cut into equal ranges, num_splits to each (sequence, key/value head) on
  * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.

@@ -183,6 +183,24 @@ int make_map(CUtensorMap* map, const void* ptr, int64_t rows, int H, int d, int 
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+// Tensor map over a [rows, H, d] bf16 tensor for the forward's padded-cache
+// variant, coordinates (channel, head of a pack, pack, row): boxes of 64 columns
+// by the 2^pack heads of a pack by 128 / 2^pack rows, 128-byte swizzle, zero fill
+// outside.
+int make_map_packed(CUtensorMap* map, const void* ptr, int64_t rows, int H, int d, int pack) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), cuuint64_t{1} << pack,
+                          static_cast<cuuint64_t>(H >> pack), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, (static_cast<cuuint64_t>(d) * 2) << pack,
+                             static_cast<cuuint64_t>(H) * static_cast<cuuint64_t>(d) * 2};
+    cuuint32_t box[4] = {64, 1u << pack, 1, 128u >> pack};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 // Tensor map over a padded cache [B, rows, H, d] bf16 tensor, coordinates
 // (channel, head, row, sequence); boxes of 64 channels x 1 head x box_rows
 // rows x 1 sequence (the same shared-memory layout as make_map's boxes),
@@ -396,6 +414,21 @@ int launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const fa::Decode
                         : FA_OK;
 }
 
+// log2 of the query heads that a chunk's blocks pack: those that share a
+// key/value head, as far as a power of two (at most a tile's 128 rows) divides
+// them.
+int chunk_pack(int64_t rows_q, int group) {
+    int pack = 0;
+    while (pack < 7 && group % (2 << pack) == 0 && (rows_q << (pack + 1)) <= (int64_t{1} << 31) - 1) ++pack;
+    return pack;
+}
+
+// Blocks of 256 rows of a chunk.
+int64_t chunk_blocks(int B, int H, int group, int Nq) {
+    const int pack = chunk_pack(static_cast<int64_t>(B) * Nq, group);
+    return static_cast<int64_t>(B) * (H >> pack) * (((static_cast<int64_t>(Nq) << pack) + 255) / 256);
+}
+
 // A chunk of queries against a padded bf16 cache with H / group heads: the
 // tensor-core forward, split along the keys when ns > 1 (partials in `part`).
 int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, int B, int H,
@@ -412,14 +445,15 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
     const int map_rows_k = rows_k > 0 ? Nk : Nq;
     if (static_cast<int64_t>(map_rows_k) * Hk * d * 2 >= (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
     CUtensorMap mq, mk, mv;
-    if (make_map(&mq, q, rows_q, H, d, 128) || make_map_cache(&mk, kk, B, map_rows_k, Hk, d, 128) ||
+    const int pack = chunk_pack(rows_q, group);
+    if (make_map_packed(&mq, q, rows_q, H, d, pack) || make_map_cache(&mk, kk, B, map_rows_k, Hk, d, 128) ||
         make_map_cache(&mv, vv, B, map_rows_k, Hk, d, 128))
         return FA_ERR_CUDA;
     fa::FwdParams p;
     p.g.B = B;
-    p.g.H = H;
-    p.g.N = Nq;
-    p.g.T = static_cast<int>(rows_q);
+    p.g.H = H >> pack;
+    p.g.N = Nq << pack;
+    p.g.T = static_cast<int>(rows_q << pack);
     p.g.cu_seqlens = nullptr;
     p.g.causal = causal ? 1 : 0;
     p.g.window = window > 0 ? window : 0;
@@ -432,13 +466,14 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
     p.error_word = st->error_word;
     p.timeout_ns = g_fault_timeout_ns ? g_fault_timeout_ns : kDefaultTimeoutNs;
     p.fault_skip_v = 0;
-    p.nsplit = static_cast<short>(ns);
+    p.nsplit = static_cast<unsigned char>(ns);
+    p.pack = static_cast<unsigned char>(pack);
     p.kv.seqused_k = seqlens_k;
     p.kv.o_part = ns > 1 ? part : nullptr;
     p.kv.lse_part = ns > 1 ? part + static_cast<size_t>(ns) * rows_q * H * d : nullptr;
-    p.group = static_cast<unsigned short>(group);
+    p.group = static_cast<unsigned short>(group >> pack);
     int grid = st->num_sms;
-    const int64_t items = static_cast<int64_t>(B) * H * ns * ((Nq + 255) / 256);
+    const int64_t items = chunk_blocks(B, H, group, Nq) * ns;
     if (items < grid) grid = static_cast<int>(items);
     const int slot = prof_start(0, stream);
     const int rc = d == 64 ? launch_fwd_cache<64>(mq, mk, mv, p, grid, stream)
@@ -504,22 +539,19 @@ Kv4Plan kv4_plan(int B, int Hkv, int Nq, int group, int Nk, int window, int num_
 }
 
 // Whether attention over the 4-bit cache multiplies the codes as they are, or
-// reads the rows back for the forward, whose blocks hold 256 queries of one head.
-// A problem that clusters take is short enough for the codes in any case: the
-// read-back's three launches alone cost as much.  Beyond that the codes' time
-// goes with the rows, Nq * group, and the read-back's with the blocks of the
-// group's heads, whatever they hold, and with the rows read back; with few tiles
-// the merge of many short items weighs on the codes.  Measured (us, codes / read
-// back), 8 kv heads, d 128.  Clusters: B 1, 512 cache rows, 512 queries 13 / 18,
-// group 4 and 100 queries 11 / 17; B 1, 2000 rows, group 4 and 70 queries 19 / 23.
-// B 16, 4096 rows: group 1 and 64 queries 75 / 106, 100 queries 119 / 106; group 4
-// and 50 queries 205 / 246, 70 queries 277 / 246; group 8 and 40 queries 308 / 403,
-// 64 queries 479 / 406.  Few tiles, B 4, 1024 rows: group 4 and 50 queries 35 /
-// 26, group 1 and 150 queries 31 / 24.
+// reads the rows back for the forward, whose blocks hold 256 rows.  A problem that
+// clusters take is short enough for the codes in any case: the read-back's three
+// launches alone cost as much.  Beyond that the codes' time goes with the rows,
+// Nq * group, and the read-back's with the blocks of a key/value head's rows and
+// with the rows read back; with few tiles the merge of many short items weighs on
+// the codes.  Measured (us, codes / read back), 8 kv heads, d 128.  Clusters: B 1,
+// 512 cache rows, 512 queries 13 / 18, group 4 and 100 queries 11 / 17; B 1, 2000
+// rows, group 4 and 70 queries 19 / 26.  B 16, 4096 rows: 64 queries 74 / 105, 100
+// queries 119 / 105; group 4 and 20 queries 89 / 105, 32 queries 136 / 105.  Few
+// tiles, B 4, 1024 rows: 150 queries 31 / 26, group 4 and 50 queries 35 / 25.
 bool kv4_direct(int B, int Hkv, int Nq, int group, int Nk, int window, int num_sms) {
     const int64_t rows = static_cast<int64_t>(Nq) * group;
-    const int64_t blocks = static_cast<int64_t>(group) * ((Nq + 255) / 256);
-    return Nk == 0 || rows <= (kv4_tiles(Nq, Nk, window) >= 32 ? 48 : 36) * (1 + blocks) ||
+    return Nk == 0 || rows <= (kv4_tiles(Nq, Nk, window) >= 32 ? 48 : 36) * (1 + chunk_blocks(1, group, group, Nq)) ||
            kv4_plan(B, Hkv, Nq, group, Nk, window, 0, num_sms).cluster > 0;
 }
 
@@ -537,15 +569,14 @@ size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
 }
 
 // Ranges that a chunk's keys are cut into: as many as the SMs hold blocks of 256
-// queries at once, never more (a second round of blocks costs as much as the
-// first), of 4 key tiles of 128 at least, and one below 16 tiles (B 4, 8 heads,
-// 1024 rows, 512 queries: 28 for one, 32 for two).  Measured (us, for 1, 2, 4, 5, 8
-// ranges), 8 kv heads, 16384 rows, d 128: group 4 and 100 queries (32 blocks)
-// 240, 134, 81, 121, 87; 512 queries (64 blocks) 244, 147, 156, 190, 177; group 1
-// and 512 queries (16 blocks) 241, 138, 85, 76, 61, and 85 for 10; B 2, 16 heads,
-// 4096 rows, 1000 queries (128 blocks) 79, 98, 116, 131, 147.
-int kv4_chunk_splits(int B, int H, int Nq, int Nk, int window, int num_sms) {
-    const int64_t items = static_cast<int64_t>(B) * H * ((Nq + 255) / 256);
+// rows at once, never more (a second round of blocks costs as much as the first),
+// of 4 key tiles of 128 at least, and one below 16 tiles (B 4, 8 heads, 1024 rows,
+// 512 queries: 28 for one, 32 for two).  Measured (us, for 1, 2, 4, 5, 8, 10
+// ranges), 8 kv heads, 16384 rows, d 128: 512 queries (16 blocks) 241, 137, 85, 76,
+// 60, 86; group 4 and 512 queries (64 blocks) 242, 145, 155, 187, 175, 183; B 2, 16
+// heads, 4096 rows, 1000 queries (128 blocks) 80, 98, 114, 129, 143, 167.
+int kv4_chunk_splits(int B, int H, int Hkv, int Nq, int Nk, int window, int num_sms) {
+    const int64_t items = chunk_blocks(B, H, H / Hkv, Nq);
     const int64_t keys = window > 0 ? std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq) : Nk;
     const int64_t tiles = (keys + 127) / 128;
     const int64_t most = tiles < 16 ? 1 : std::min<int64_t>(fa::kDecMaxSplits, tiles / 4);
@@ -557,7 +588,7 @@ int kv4_chunk_splits(int B, int H, int Nq, int Nk, int window, int num_sms) {
 size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const int group = H / Hkv;
     if (!kv4_direct(B, Hkv, Nq, group, Nk, window, num_sms))
-        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Nq, Nk, window, num_sms));
+        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Hkv, Nq, Nk, window, num_sms));
     const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms);
     const size_t rows = 2 * static_cast<size_t>(plan.ranges) * plan.block_rows;
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
@@ -771,7 +802,7 @@ int fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float* lse, 
     if (!packed && Nk > 0 && Nk >= 2 * static_cast<int64_t>(Nq)) {
         CUtensorMap mq, mk, mv;
         if (static_cast<int64_t>(Nk) * H * d * 2 >= (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
-        if (make_map(&mq, q, c.rows, H, d, 128) || make_map_cache(&mk, k, B, Nk, H, d, 128) ||
+        if (make_map_packed(&mq, q, c.rows, H, d, 0) || make_map_cache(&mk, k, B, Nk, H, d, 128) ||
             make_map_cache(&mv, v, B, Nk, H, d, 128))
             return FA_ERR_CUDA;
         fa::FwdParams p;
@@ -786,6 +817,7 @@ int fa_fwd_kv(const void* q, const void* k, const void* v, void* o, float* lse, 
         p.kv.seqused_k = nullptr;
         p.kv.o_part = nullptr;
         p.kv.lse_part = nullptr;
+        p.pack = 0;
         p.group = 1;
         int grid = st->num_sms;
         const int64_t items = static_cast<int64_t>(B) * H * ((Nq + 255) / 256);
@@ -974,7 +1006,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
     if (!kv4_direct(B, Hkv, Nq, group, Nk, window, num_sms)) {
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
-        const int ns = num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Nq, Nk, window, num_sms);
+        const int ns = num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Hkv, Nq, Nk, window, num_sms);
         uint8_t* back = static_cast<uint8_t*>(workspace) + decode_workspace_bytes(B, H, Nq, d, ns);
         void* kb = back;
         void* vb = back + kv4_readback_bytes(B, Hkv, Nk, d);

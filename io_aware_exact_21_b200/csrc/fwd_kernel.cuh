@@ -52,8 +52,10 @@
 // each item then writes O / l as fp32 and the base-2 log-sum-exp of its range
 // to the split buffers ([nsplit, rows, H, D] and [nsplit, H, rows]), which
 // combine_kernel merges.  A split with no tiles writes -inf and is skipped by
-// the merge.  Query head h reads key/value head h / group (group = 1 where
-// every query head has its own).  Cache rows past a sequence's used length are never read: K and V
+// the merge.  Query heads may share a key/value head: 2^pack of them are packed
+// into one item's rows, query i's next to each other (the Q map brings them in
+// so, and the geometry has N 2^pack rows and H / 2^pack heads of them), and
+// `group` such heads read one key/value head.  Cache rows past a sequence's used length are never read: K and V
 // come through 4-D maps [B, Nk, H, d] (coordinates channel, head, row,
 // sequence), and a key tile that would reach past the used length nk is read
 // right-aligned instead, as keys [nk - 128, nk) -- rows before 0 are outside
@@ -104,8 +106,9 @@ struct FwdParams {
     union {
         int nb;                 // FP8
         struct {                // padded cache
-            short nsplit;
-            unsigned short group;   // query heads to a key/value head (the maps' heads: H / group)
+            unsigned char nsplit;
+            unsigned char pack;     // log2 of the query heads whose rows one item holds, row i * 2^pack + head
+            unsigned short group;   // items' heads (g.H of them) to a key/value head
         };
     };
 };
@@ -249,6 +252,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const uint32_t tmem = *tmem_holder;
     const WaitCtl wc{abort_flag, p.error_word, p.timeout_ns};
     const int H = p.g.H;
+    const int pack = kCache ? p.pack : 0;
 
     // register split: 120 per thread for the producer / MMA warpgroup, 192 for
     // the two softmax warpgroups: 120 * 128 + 192 * 256 = 64512, the launch's
@@ -274,11 +278,11 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 [[maybe_unused]] const int hk = kCache ? h / p.group : h;
                 const SeqSpan sp = sch.span(s);
                 const SeqSpan kp = kCache ? sch.kspan_used(s, p.kv.seqused_k) : sch.kspan(s);
-                const int off = kp.len - sp.len;        // key position of query row 0
+                const int off = kp.len - (sp.len >> pack);      // key position of query row 0
                 const int r_lo = blk * C::ROWS;
                 const int r_hi = min(sp.len, r_lo + C::ROWS);
                 int jb, je;
-                key_tile_range(r_lo + off, r_hi + off, kp.len, p.g.causal, p.g.window, C::BN, jb, je);
+                key_tile_range((r_lo >> pack) + off, ((r_hi - 1) >> pack) + 1 + off, kp.len, p.g.causal, p.g.window, C::BN, jb, je);
                 if constexpr (kCache) {
                     if (!split_tile_range(p.nsplit, split, jb, je)) {
                         --item_it;          // no tiles: no barrier phase for this item
@@ -294,9 +298,14 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 if (!mbar_wait(q_empty, (item_it & 1) ^ 1, wc)) { ok = false; break; }
                 mbar_arrive_expect_tx(q_full, 2 * C::TILE_BYTES);
                 for (int t = 0; t < 2; ++t)
-                    for (int b = 0; b < C::NBOX; ++b)
-                        tma_load_3d(sQ + t * C::TILE_BYTES + b * C::BOX_BYTES, &tm_q, q_full,
-                                    b * 128 / C::ESIZE, h, sp.start + r_lo + t * C::BM);
+                    for (int b = 0; b < C::NBOX; ++b) {
+                        uint8_t* dst = sQ + t * C::TILE_BYTES + b * C::BOX_BYTES;
+                        if constexpr (kCache)
+                            tma_load_4d(dst, &tm_q, q_full, b * 128 / C::ESIZE, 0, h,
+                                        (sp.start + r_lo + t * C::BM) >> pack);
+                        else
+                            tma_load_3d(dst, &tm_q, q_full, b * 128 / C::ESIZE, h, sp.start + r_lo + t * C::BM);
+                    }
                 ++q_issued;
                 for (int j = jb; j < je && ok; ++j) {
                     for (int kv = 0; kv < 2; ++kv) {
@@ -440,11 +449,12 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 }
                 const SeqSpan sp = sch.span(s);
                 const SeqSpan kp = kCache ? sch.kspan_used(s, p.kv.seqused_k) : sch.kspan(s);
-                const int off = kp.len - sp.len;
+                const int off = kp.len - (sp.len >> pack);
                 const int r_lo = blk * C::ROWS;
                 const int r_hi = min(sp.len, r_lo + C::ROWS);
                 int jb, je;
-                key_tile_range(r_lo + off, r_hi + off, kp.len, p.g.causal, p.g.window, C::BN, jb, je);
+                key_tile_range((r_lo >> pack) + off, ((r_hi - 1) >> pack) + 1 + off, kp.len, p.g.causal,
+                               p.g.window, C::BN, jb, je);
                 if constexpr (kCache) {
                     if (!split_tile_range(p.nsplit, split, jb, je)) {
                         --item_it;          // no tiles: no barrier phase for this item
@@ -536,17 +546,21 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             const SeqSpan kp = kCache ? sch.kspan_used(s, p.kv.seqused_k) : sch.kspan(s);
             const int n = sp.len;
             const int nk = kp.len;
-            const int off = nk - n;                     // key position of query row 0
+            const int off = nk - (n >> pack);           // key position of query row 0
             const int r_lo = blk * C::ROWS;
             const int r_hi = min(n, r_lo + C::ROWS);
             int jb, je;
-            key_tile_range(r_lo + off, r_hi + off, nk, p.g.causal, p.g.window, C::BN, jb, je);
+            key_tile_range((r_lo >> pack) + off, ((r_hi - 1) >> pack) + 1 + off, nk, p.g.causal,
+                           p.g.window, C::BN, jb, je);
             const int r0 = r_lo + t * C::BM;            // first row of this tile
             const int i = r0 + row_in_tile;             // this thread's row
+            // its place in the outputs: token row, head, and how many there are
+            [[maybe_unused]] const int out_row = (sp.start + i) >> pack, out_T = p.g.T >> pack;
+            [[maybe_unused]] const int out_h = (h << pack) + (i & ((1 << pack) - 1)), out_H = H << pack;
             if constexpr (kCache) {
                 if (!split_tile_range(p.nsplit, split, jb, je)) {
                     if (i < n)
-                        p.kv.lse_part[(static_cast<size_t>(split) * H + h) * p.g.T + sp.start + i] =
+                        p.kv.lse_part[(static_cast<size_t>(split) * out_H + out_h) * out_T + out_row] =
                             -INFINITY;
                     --item_it;
                     continue;
@@ -588,7 +602,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                     for (int e = 0; e < C::BN; ++e) sv[e] = __uint_as_float(r[e]);
                 }
                 const int k0 = j * C::BN;
-                const bool masked = tile_needs_mask_pos(r0 + off, min(r0 + C::BM, n) + off, k0, C::BN,
+                const bool masked = tile_needs_mask_pos((r0 >> pack) + off,
+                                                        ((min(r0 + C::BM, n) - 1) >> pack) + 1 + off, k0, C::BN,
                                                         nk, p.g.causal, p.g.window);
                 if (masked) {
                     // this row's allowed keys of the tile are columns [c_lo, c_hi)
@@ -597,7 +612,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                         // the tile holds keys from k0r on; those below k0 belong to
                         // the tile before it
                         const int k0r = cache_tile_key0(j, nk);
-                        tile_key_bounds(i + off, k0r, nk, p.g.causal, p.g.window, C::BN, c_lo, c_hi);
+                        tile_key_bounds((i >> pack) + off, k0r, nk, p.g.causal, p.g.window, C::BN, c_lo, c_hi);
                         c_lo = max(c_lo, min(k0 - k0r, C::BN));
                         c_hi = max(c_hi, c_lo);
                     } else {
@@ -688,7 +703,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             const float inv_l = l > 0.f ? (kF8 ? sv_max : 1.f) / l : 0.f;
             if constexpr (kCache) if (p.nsplit > 1) {
                 // this split's O / l (fp32) and base-2 log-sum-exp
-                float* prow = p.kv.o_part + ((static_cast<size_t>(split) * p.g.T + sp.start + i) * H + h) * D;
+                float* prow = p.kv.o_part +
+                              ((static_cast<size_t>(split) * out_T + out_row) * out_H + out_h) * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
@@ -706,20 +722,22 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 }
                 if (valid)
                     // (a NaN sum stays NaN, so that the merge does not pass over this split)
-                    p.kv.lse_part[(static_cast<size_t>(split) * H + h) * p.g.T + sp.start + i] =
+                    p.kv.lse_part[(static_cast<size_t>(split) * out_H + out_h) * out_T + out_row] =
                         l == 0.f ? -INFINITY : m_ref + __log2f(l);
                 tc_fence_before();
                 continue;
             }
-            __nv_bfloat16* orow = p.o + (static_cast<size_t>(sp.start) + i) * H * D +
-                                  static_cast<size_t>(h) * D;
+            __nv_bfloat16* orow = p.o + (kCache ? (static_cast<size_t>(out_row) * out_H + out_h) * D
+                                                : (static_cast<size_t>(sp.start) + i) * H * D +
+                                                      static_cast<size_t>(h) * D);
             // 64 columns (one 128-byte line of the row) at a time, whole lines
             // per store instruction
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) store_line_bf16(tO + c * 64, inv_l, orow + c * 64, valid);
             if (valid) {
                 const float lse = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
-                const size_t idx = p.g.cu_seqlens
+                const size_t idx = kCache ? (static_cast<size_t>(s) * out_H + out_h) * (p.g.N >> pack) + (i >> pack)
+                                   : p.g.cu_seqlens
                                        ? static_cast<size_t>(h) * p.g.T + sp.start + i
                                        : (static_cast<size_t>(s) * H + h) * p.g.N + i;
                 p.lse[idx] = lse;

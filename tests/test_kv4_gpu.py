@@ -347,7 +347,9 @@ CHUNKS = [(2, 40, 2, 2, 304, 128), (1, 129, 6, 2, 1000, 64), (2, 300, 4, 1, 520,
           (1, 600, 2, 1, 2048, 128), (2, 96, 2, 2, 304, 64), (2, 97, 2, 2, 304, 64), (1, 33, 64, 1, 136, 128),
           # more blocks of 16 rows than run at once, and rows enough for the forward over the rows read back
           (2, 310, 8, 2, 520, 128), (3, 420, 4, 4, 1000, 64), (2, 150, 16, 16, 304, 128), (40, 97, 8, 8, 136, 64),
-          (1, 1200, 8, 2, 136, 128)]
+          (1, 1200, 8, 2, 136, 128),
+          # groups of 3, 6, 16 and 256 heads: 1, 2, 16 and 128 of them share a block's rows
+          (3, 250, 12, 4, 304, 64), (2, 200, 24, 4, 304, 128), (1, 100, 128, 8, 304, 64), (1, 40, 256, 1, 136, 64)]
 
 
 @pytest.mark.parametrize("B,Nq,H,Hkv,Nk,d", CHUNKS)
