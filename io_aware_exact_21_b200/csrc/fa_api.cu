@@ -588,7 +588,8 @@ int kv4_chunk_splits(int B, int H, int Hkv, int Nq, int Nk, int window, int num_
 size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
     const int group = H / Hkv;
     if (!kv4_direct(B, Hkv, Nq, group, Nk, window, num_sms))
-        return decode_workspace_bytes(B, H, Nq, d, num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Hkv, Nq, Nk, window, num_sms));
+        return decode_workspace_bytes(
+            B, H, Nq, d, num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Hkv, Nq, Nk, window, num_sms));
     const Kv4Plan plan = kv4_plan(B, Hkv, Nq, group, Nk, window, num_splits, num_sms);
     const size_t rows = 2 * static_cast<size_t>(plan.ranges) * plan.block_rows;
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
@@ -614,7 +615,7 @@ bool kv4_bad_attention(int B, int H, int Hkv, int Nq, int Nk, int d, int window,
     if (rows_q == 0) return false;
     if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms)) return H / Hkv > 65535;
     return rows_q * H > kMax ||      // a CTA each in the merge; the key tiles are counted in 32 bits
-           static_cast<int64_t>(B) * Hkv * (Nk / 32 + 1) * kv4_row_blocks(rows) > kMax;
+           static_cast<int64_t>(B) * Hkv * (Nk / 32 + 2) * kv4_row_blocks(rows) > kMax;
 }
 
 // Writes (kWrite) or reads the rows of p.place, K and V in one launch.
