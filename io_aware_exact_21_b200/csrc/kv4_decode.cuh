@@ -18,7 +18,14 @@
 // down to 2^-24 of that one and off by 2^-25 of the row's largest below it;
 // p s^v is scaled likewise by the largest s^v of the warp's keys so far and
 // rounded to fp16 (2^-11; the two-byte operand the product needs, finer than
-// bf16's 2^-8).  Everything else is fp32, the row sums take the unrounded p.
+// bf16's 2^-8).  The zeros are one more row of the second product, so the same
+// rounded weights multiply c and z, and an error of theirs goes with |c - z|: with
+// the weights as they were before the rounding it went with c, eight times as far
+// where most codes stand next to z.  (The products themselves are exact, but the
+// tensor core takes an fp16 subnormal for a number of 2^-14 when it lines products up
+// to add them, and cuts what lies 2^-23 below the largest: up to 2^-13 of the largest
+// w of 16 keys, in units of a code.  z is cut as c is.)  Everything else is fp32, the row sums take
+// the unrounded p.
 //
 // What bounds it: with R = Nq * H / Hkv query rows to a key/value head the
 // cache is D + 4 bytes a token and head for 4 R D operations, so up to a dozen
@@ -87,11 +94,11 @@ struct Kv4DecCfg {
     static constexpr int TILE = BN * ROWB;                // K or V codes of a tile
     static constexpr int WORDB = BN * 2;
     // a warp's shared memory: V codes (swizzled, so 1024-byte aligned); K codes,
-    // K words, V words; (scale, zero) of K and V
+    // K words, V words; (scale, zero) of K, scales of V, zeros of V as 16-bit words
     static constexpr int OFF_K = TILE;
     static constexpr int OFF_WORDS = OFF_K + TILE;
     static constexpr int OFF_SCALES = OFF_WORDS + 2 * WORDB;
-    static constexpr int WARP_BYTES = (OFF_SCALES + 2 * BN * 8 + 1023) / 1024 * 1024;
+    static constexpr int WARP_BYTES = (OFF_SCALES + BN * 14 + 1023) / 1024 * 1024;
     static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][2]: K, V
     static constexpr int OFF_MISC = OFF_BAR + WARPS * 16;
     static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16 + 1024;
@@ -207,12 +214,13 @@ struct Kv4Row {
 };
 
 // What a warp has of an item: O^T in mma fragments ([m][nt][mma row g8 / g8 + 8],
-// query rows 2 t4 + {0, 1}), the lane's sums of p and of p s^v z, minus the
-// reference (kNoRef: none), the exponent that O and za are scaled by.
+// query rows 2 t4 + {0, 1}), the sums of p s^v z likewise (mma rows 0 .. 7 alike,
+// for the even channels, and 8 .. 15), the lane's sums of p, minus the reference (kNoRef: none), the exponent that O
+// and za are scaled by.
 template <int D, int NT>
 struct Kv4Acc {
-    float2 o[D / 16][NT][2];
-    float2 l[NT], za[NT], nm[NT];
+    float2 o[D / 16][NT][2], za[NT][2];
+    float2 l[NT], nm[NT];
     uint32_t ev;                    // biased exponent of the largest V scale
 };
 
@@ -230,7 +238,8 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
     const float kNegInf = -INFINITY;
     uint64_t* bar_v = bar_k + 1;
     float2* sck = reinterpret_cast<float2*>(ring + C::OFF_SCALES);
-    float2* scv = sck + C::BN;
+    float* scv = reinterpret_cast<float*>(sck + C::BN);
+    uint16_t* zv = reinterpret_cast<uint16_t*>(scv + C::BN);
     const int qpos0 = nk - p.Nq;                             // key position of query 0
     const int64_t row0 = (static_cast<int64_t>(b) * p.Hkv + hk) * p.Nk + static_cast<int64_t>(first) * C::BN;
     const int room = p.Nk - first * C::BN;
@@ -259,6 +268,9 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
     const uint32_t v_at = smem_u32(ring) + v_key / KPL * 128 +
                           ((((v_key % KPL) * (8 / KPL)) | (lane >> 4)) ^ (v_key / KPL)) * 16;
     const int kkey = kv4_key(g8);
+    // the keys of the lane's code pairs in the second product: these two and the
+    // two that are 4 further
+    const uint16_t* zv_at = zv + (t4 >> 1) * 8 + (t4 & 1) * 2;
     if (count > 0) {
         if (!p.fault_skip) load_k(0);
         load_v(0);
@@ -324,12 +336,23 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
     const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
 
     float2 (&oacc)[D / 16][NT][2] = acc.o;
-    float2 (&l)[NT] = acc.l, (&za)[NT] = acc.za, (&nm)[NT] = acc.nm;
+    float2 (&za)[NT][2] = acc.za;
+    float2 (&l)[NT] = acc.l, (&nm)[NT] = acc.nm;
+    // O and za of a nt times f
+    auto scale_rows = [&](int nt, float2 f) {
+        za[nt][0] = fmul2(za[nt][0], f);
+        za[nt][1] = fmul2(za[nt][1], f);
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) {
+            oacc[m][nt][0] = fmul2(oacc[m][nt][0], f);
+            oacc[m][nt][1] = fmul2(oacc[m][nt][1], f);
+        }
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) oacc[m][nt][0] = oacc[m][nt][1] = make_float2(0.f, 0.f);
-        l[nt] = za[nt] = make_float2(0.f, 0.f);
+        l[nt] = za[nt][0] = za[nt][1] = make_float2(0.f, 0.f);
         nm[nt] = make_float2(kNoRef, kNoRef);
     }
     uint32_t& ev = acc.ev;
@@ -371,14 +394,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
             if (top > ev) {         // a larger scale than any before: O goes down with the new factor
                 const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    za[nt] = fmul2(za[nt], make_float2(d, d));
-#pragma unroll
-                    for (int m = 0; m < D / 16; ++m) {
-                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], make_float2(d, d));
-                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], make_float2(d, d));
-                    }
-                }
+                for (int nt = 0; nt < NT; ++nt) scale_rows(nt, make_float2(d, d));
                 ev = top;
                 vnorm = __uint_as_float((260u - ev) << 23);
             }
@@ -386,8 +402,8 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
             for (int kk = 0; kk < C::BN / 32; ++kk) {
                 sck[kk * 32 + lane] = make_float2(__uint_as_float((wk[kk] & 0xfff0u) << 16),
                                                   __uint_as_float(0x4b000000u | (wk[kk] & 15u)) - 8388608.f);
-                scv[kk * 32 + lane] = make_float2(__uint_as_float((wv[kk] & 0xfff0u) << 16) * vnorm,
-                                                  __uint_as_float(0x4b000000u | (wv[kk] & 15u)) - 8388608.f);
+                scv[kk * 32 + lane] = __uint_as_float((wv[kk] & 0xfff0u) << 16) * vnorm;
+                zv[kk * 32 + lane] = static_cast<uint16_t>(wv[kk] & 15u);       // fp16: z 2^-24, as the codes
             }
         }
         __syncwarp();
@@ -478,12 +494,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
                                                  nm[nt].y == kNoRef ? 0.f : ex2(n2.y - nm[nt].y));
                     nm[nt] = n2;
                     l[nt] = fmul2(l[nt], a);
-                    za[nt] = fmul2(za[nt], a);
-#pragma unroll
-                    for (int m = 0; m < D / 16; ++m) {
-                        oacc[m][nt][0] = fmul2(oacc[m][nt][0], a);
-                        oacc[m][nt][1] = fmul2(oacc[m][nt][1], a);
-                    }
+                    scale_rows(nt, a);
                 }
             }
             bool over = false;
@@ -512,14 +523,22 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         for (int m = 0; m < C::MT; ++m)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float2 sz = scv[m * 16 + half * 4 + kkey];
+                const float sv = scv[m * 16 + half * 4 + kkey];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float2 w = fmul2(e[m][nt][half], make_float2(sz.x, sz.x));
-                    za[nt] = ffma2(w, make_float2(sz.y, sz.y), za[nt]);
+                    const float2 w = fmul2(e[m][nt][half], make_float2(sv, sv));
                     pf[m][nt][half] = transpose8x8(pack_f16(w.x, w.y));
                 }
             }
+        // ---- za += Z (p s^v)^T: the zeros, at the places of a byte's low code and
+        // of its high one, so that the products lose the same as those of O
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) {
+            const uint32_t z0 = *reinterpret_cast<const uint32_t*>(zv_at + m * 16);
+            const uint32_t z1 = *reinterpret_cast<const uint32_t*>(zv_at + m * 16 + 4);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(za[nt], z0, z0 << 4, z1, z1 << 4, pf[m][nt][0], pf[m][nt][1]);
+        }
         // ---- O^T += C^v (p s^v)^T
         if (!__all_sync(0xffffffffu, mbar_wait(bar_v, phase, wc))) return false;
 #pragma unroll
@@ -558,19 +577,18 @@ __device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, int nrows, cons
         for (int o = 4; o <= 16; o <<= 1) {
             acc.l[nt].x += __shfl_xor_sync(0xffffffffu, acc.l[nt].x, o);
             acc.l[nt].y += __shfl_xor_sync(0xffffffffu, acc.l[nt].y, o);
-            acc.za[nt].x += __shfl_xor_sync(0xffffffffu, acc.za[nt].x, o);
-            acc.za[nt].y += __shfl_xor_sync(0xffffffffu, acc.za[nt].y, o);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = nt * 8 + 2 * t4 + j;
             if (r >= nrows) continue;
-            const float z = j ? acc.za[nt].y : acc.za[nt].x, n1 = j ? acc.nm[nt].y : acc.nm[nt].x;
+            const float z0 = j ? acc.za[nt][0].y : acc.za[nt][0].x, z1 = j ? acc.za[nt][1].y : acc.za[nt][1].x;
+            const float n1 = j ? acc.nm[nt].y : acc.nm[nt].x;
             float a[D / 8];
 #pragma unroll
             for (int m = 0; m < D / 16; ++m) {      // codes times 2^-24, and 2^-20
-                a[2 * m] = fmaf(j ? acc.o[m][nt][0].y : acc.o[m][nt][0].x, 16777216.f, -z) * back;
-                a[2 * m + 1] = fmaf(j ? acc.o[m][nt][1].y : acc.o[m][nt][1].x, 1048576.f, -z) * back;
+                a[2 * m] = ((j ? acc.o[m][nt][0].y : acc.o[m][nt][0].x) - z0) * 16777216.f * back;
+                a[2 * m + 1] = ((j ? acc.o[m][nt][1].y : acc.o[m][nt][1].x) - z1) * 1048576.f * back;
             }
             put(r, a, n1 == kNoRef ? -INFINITY : -n1, j ? acc.l[nt].y : acc.l[nt].x);
         }

@@ -1,0 +1,133 @@
+"""Attention over the 4-bit cache where the rows' weights p s^v differ much, or
+hardly at all: against 64 bits, within bounds that go by |c - z|, what a row
+stands for, not by c and z apart."""
+import math
+
+import pytest
+import torch
+
+import io_aware_exact_21_b200 as fa
+from test_kv4_gpu import DEV, queries, random_cache, stands_for
+
+pytestmark = pytest.mark.gpu
+
+
+def scales(words):
+    return (words & -16).view(torch.bfloat16).double()
+
+
+def tight_reference(q, cache, lens, causal, window, scale):
+    """(O, LSE, bound of |O error|) in float64, for the kernels that multiply the
+    codes.
+
+    Bounds.  x: each score is off by at most e = (d + 8) 2^-24 A (A = scale s_j
+    sum |q| (c + z), the largest of the row) + 2^-21 (the exponential); the sum
+    over n keys adds n 2^-24; so a normalised weight is off by 4 e relative at
+    most, as in test_kv4_gpu.  w_j = p_j s^v_j is rounded to fp16: by 2^-11 of
+    itself, or where it is small by 2^-21 of the row's largest w (the kernel
+    keeps a row's largest above 2^-4, and fp16's smallest step is 2^-24).  The same
+    rounded w multiply c and z, so both errors reach O times |c - z|: 2^-11
+    sum p |v| and 2^-21 max w sum |c - z|.  The tensor core adds 16 products and
+    the sum so far cut off 2^-23 below the largest; a code is an fp16 subnormal,
+    whose product w c 2^-24 counts there as one of w 2^-14: in units of a code, 18
+    2^-13 of the largest w of the 16, cut the same way for c and z, and 2^-23 of the
+    sums, sum w (c + z), in each of n / 16 steps.  O is rounded to bf16: 2^-8.
+    """
+    B, Nq, H, d = q.shape
+    G = H // cache["k_codes"].shape[1]
+    O = torch.zeros((B, Nq, H, d), dtype=torch.float64, device=DEV)
+    L = torch.full((B, H, Nq), -math.inf, dtype=torch.float64, device=DEV)
+    bo = torch.zeros_like(O)
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        pos = torch.arange(n - Nq, n, device=DEV)[:, None]
+        j = torch.arange(n, device=DEV)[None]
+        ok = torch.ones((Nq, n), dtype=torch.bool, device=DEV)
+        if causal:
+            ok &= j <= pos
+        if window > 0:
+            ok &= j > pos - window
+        for h in range(H):
+            kc, kw = cache["k_codes"][b, h // G, :n], cache["k_words"][b, h // G, :n]
+            vc, vw = cache["v_codes"][b, h // G, :n], cache["v_words"][b, h // G, :n]
+            kk, vv, sv = stands_for(kc, kw), stands_for(vc, vw), scales(vw)
+            qq = q[b, :, h].double()
+            x = torch.where(ok, scale * (qq @ kk.T), -math.inf)
+            some = ok.any(-1)
+            L[b, h] = torch.logsumexp(x, -1)
+            p = torch.where(ok, torch.exp(x - torch.where(some, L[b, h], 0.0)[:, None]), 0.0)
+            O[b, :, h] = p @ vv
+            both = lambda c, w: (torch.stack((c & 15, c >> 4), -1).flatten(-2).double()  # noqa: E731
+                                 + (w & 15).double()[:, None])
+            A = torch.where(ok, scale * (qq.abs() @ (scales(kw)[:, None] * both(kc, kw)).T), 0.0).amax(-1)
+            e = (d + 8) * 2.0 ** -24 * A + 2.0 ** -21 + n * 2.0 ** -24
+            w = p * sv
+            steps = torch.where(sv[:, None] > 0, (vv / sv.clamp(min=2.0 ** -133)[:, None]).abs(), 0.0)
+            bo[b, :, h] = (2.0 ** -8 * O[b, :, h].abs() + 1.01 * (
+                (2.0 ** -11 + 4 * e)[:, None] * (p @ vv.abs())
+                + 2.0 ** -21 * w.amax(-1, keepdim=True) * (ok.double() @ steps)
+                + 18 * 2.0 ** -13 * (torch.nn.functional.pad(w, (0, -n % 16)).view(Nq, -1, 16)).amax(-1).sum(-1)[:, None]
+                + (n / 16 + 1) * 2.0 ** -23 * (w @ both(vc, vw))))
+    return O, L, bo
+
+
+def runs_on_the_codes(q, cache, window, num_splits):
+    B, Nq, H, d = q.shape
+    Hkv, Nk = cache["k_codes"].shape[1:3]
+    return fa.fa_fwd_kv4_workspace_size(B, H, Hkv, Nq, Nk, d, window, num_splits) < 2 * B * Nk * Hkv * d * 2
+
+
+def check(q, cache, lens, causal, window=0, num_splits=0, codes=True):
+    d = q.shape[-1]
+    O, L, bo = tight_reference(q, cache, lens.tolist(), causal, window, d ** -0.5)
+    assert not codes or runs_on_the_codes(q, cache, window, num_splits)
+    o, lse = fa.forward_kv4(q, cache, seqlens_k=lens.to(DEV), causal=causal, window=window, num_splits=num_splits)
+    assert fa.fa_get_device_error() == 0
+    assert torch.isfinite(o).all()
+    err = (o.double() - O).abs()
+    assert (err <= bo).all(), "O: %.3g of its bound" % (err / bo.clamp(min=1e-300)).max()
+    empty = torch.isneginf(L)
+    assert torch.equal(torch.isneginf(lse), empty)
+    return o, lse
+
+
+def full(lens):
+    return torch.tensor(lens, dtype=torch.int32)
+
+
+SHAPES = [  # B, Nq, H, Hkv, Nk, d
+    (2, 1, 8, 1, 1000, 128), (2, 3, 6, 2, 312, 64), (1, 16, 2, 1, 520, 128), (2, 1, 16, 1, 4096, 128),
+    # above 32 rows to a key/value head, still on the codes
+    (2, 40, 2, 2, 304, 128), (1, 33, 8, 4, 1000, 64), (1, 16, 16, 4, 2048, 128),
+]
+
+
+@pytest.mark.parametrize("B,Nq,H,Hkv,Nk,d", SHAPES)
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 100)])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_ordinary_rows(B, Nq, H, Hkv, Nk, d, causal, window, num_splits):
+    cache = random_cache(B, Nk, Hkv, d, seed=Nk + Nq)
+    check(queries(B, Nq, H, d, 7), cache, full([Nk] * B), causal, window, num_splits)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_equal_weights_of_rows_near_their_zero(d, num_splits):
+    # each V row has one channel of 15 steps and all others at 0 or one step from
+    # it, and the keys are alike, so that all weights round the same way: what
+    # the rounding does must go with |c - z| (1), not with c (7 and 8)
+    n = 512
+    g = torch.Generator("cpu").manual_seed(3)
+    v = torch.randint(-1, 2, (1, n, 1, d), generator=g).float()
+    v[..., 0], v[..., 1] = 8.0, -7.0
+    k = torch.zeros((1, n, 1, d))
+    for t in range(12):
+        # one key above the others by a little, in every warp's first tile: the
+        # others' p are then 2^-y with another fraction each time
+        k[0, ::64, 0, 0] = 0.25 + t / 8
+        cache = fa.quantize_kv4(k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), fa.kv4_cache(1, n, 1, d))
+        q = torch.zeros((1, 1, 4, d), dtype=torch.bfloat16, device=DEV)
+        q[..., 0] = torch.tensor([1.0, 2.0, 3.0, 5.0], device=DEV)
+        check(q, cache, full([n]), True, 0, num_splits)
