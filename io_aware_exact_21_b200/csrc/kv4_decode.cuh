@@ -13,19 +13,26 @@
 // into the last scaling of O.  The scales and zeros apply to the small fp32
 // score tile: scale after the product, s^v folded into p.
 //
-// Roundings: q is scaled by a power of two per row so that its largest
-// element lies in [2^14, 2^15) and held in fp16, which is exact for elements
-// down to 2^-24 of that one and off by 2^-25 of the row's largest below it;
-// p s^v is scaled likewise by the largest s^v of the warp's keys so far and
-// rounded to fp16 (2^-11; the two-byte operand the product needs, finer than
-// bf16's 2^-8).  The zeros are one more row of the second product, so the same
-// rounded weights multiply c and z, and an error of theirs goes with |c - z|: with
-// the weights as they were before the rounding it went with c, eight times as far
-// where most codes stand next to z.  (The products themselves are exact, but the
-// tensor core takes an fp16 subnormal for a number of 2^-14 when it lines products up
-// to add them, and cuts what lies 2^-23 below the largest: up to 2^-13 of the largest
-// w of 16 keys, in units of a code.  z is cut as c is.)  Everything else is fp32, the row sums take
-// the unrounded p.
+// Roundings.  q is scaled by a power of two per row so that its largest element
+// lies in [2^14, 2^15) and held in fp16, which is exact for elements down to 2^-24
+// of that one and off by 2^-25 of the row's largest below it.  w = p s^v is scaled
+// by a power of two and rounded to fp16, the two-byte operand that the product
+// needs: by 2^-11 (bf16: 2^-8) or, where it is small, by 2^-21 of the largest w of
+// its query row.  The power of two is one for the warp, from the largest s^v of its
+// keys so far, while the s^v of all keys that its rows can see lie within 2^10 of
+// that: then each row's largest w stays above 2^-4 (p is 1 at the row's reference),
+// and fp16's step is at most 2^-24.  Where a scale lies farther off, a large row that
+// a mask hides from another query, or whose p is next to nothing, would push the w
+// that count out of fp16; from there on each query row has a power of two of its own,
+// from the largest w it has met (kv4_attend).  Looking for such scales costs a vote a
+// tile: 1 to 3 % of the time, 5 % of the shortest calls.
+// The zeros are one more row of the second product, so the same rounded weights
+// multiply c and z, and an error of theirs goes with |c - z|; with the weights as they
+// were before the rounding it went with c, eight times as far where most codes stand
+// next to z.  (The products are exact, but the tensor core takes an fp16 subnormal for
+// a number of 2^-14 when it lines products up to add them, and cuts what lies 2^-23
+// below the largest: up to 2^-13 of the largest w of 16 keys, in units of a code.  z is
+// cut as c is.)  Everything else is fp32, the row sums take the unrounded p.
 //
 // What bounds it: with R = Nq * H / Hkv query rows to a key/value head the
 // cache is D + 4 bytes a token and head for 4 R D operations, so up to a dozen
@@ -98,14 +105,41 @@ struct Kv4DecCfg {
     static constexpr int OFF_K = TILE;
     static constexpr int OFF_WORDS = OFF_K + TILE;
     static constexpr int OFF_SCALES = OFF_WORDS + 2 * WORDB;
-    static constexpr int WARP_BYTES = (OFF_SCALES + BN * 14 + 1023) / 1024 * 1024;
+    static constexpr int OFF_ROWS = OFF_SCALES + BN * 14;               // [ROWS] Kv4RowScale
+    static constexpr int WARP_BYTES = (OFF_ROWS + ROWS * 12 + 1023) / 1024 * 1024;
     static constexpr int OFF_BAR = WARPS * WARP_BYTES;                  // [WARPS][2]: K, V
     static constexpr int OFF_MISC = OFF_BAR + WARPS * 16;
     static constexpr int SMEM = OFF_MISC + WARPS * 12 + 16 + 1024;
     static constexpr int OSTRIDE = D + 4;                 // floats a row of a partial output in shared memory
     static_assert(TILE % 1024 == 0 && OFF_WORDS % 16 == 0 && WORDB % 16 == 0, "copies and swizzle");
-    static_assert(ROWS * (OSTRIDE + 2) * 4 <= WARP_BYTES, "a warp leaves its partial result in its memory");
+    static_assert(ROWS * (OSTRIDE + 2) * 4 <= OFF_ROWS, "a warp leaves its partial result in its memory");
 };
+
+// p may grow to this before its reference moves: 2^8 times s^v below 2^7 is in fp16
+constexpr float kKv4Over = 256.f;
+constexpr float kNoRef = 3.4028234e38f;   // minus the reference before the first score: any score then is over
+
+// Where the V scales of a warp's keys differ by more than kKv4Spread powers of
+// two: a query row's largest w, in units of 2^8, up to the last tile, minus the
+// reference that it is relative to (kNoRef: no key yet), and the power k that the
+// row's w and sums are scaled by in those units.
+constexpr int kKv4Spread = 10;
+constexpr uint32_t kKv4Unseen = 0x10000u;   // in place of the word of a V row that no query sees: s, z = 0
+struct Kv4RowScale {
+    float largest, minus_ref;
+    int k;
+    __device__ __forceinline__ void take(float w, float nm) {
+        largest = fmaxf(minus_ref == kNoRef ? 0.f : largest * ex2(nm - minus_ref), w);
+        minus_ref = nm;
+    }
+};
+
+// The power that brings the largest w into [2^13, 2^14); the limits keep p 2^k and
+// 2^-k within fp32.
+__device__ __forceinline__ int kv4_row_power(const Kv4RowScale& r) {
+    return min(max(r.largest > 0.f ? 140 - static_cast<int>(__float_as_uint(r.largest) >> 23) : r.k, -112), 119);
+}
+__device__ __forceinline__ float kv4_pow2(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 __device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -138,9 +172,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 
 constexpr uint32_t kNibLo = 0x000f000fu, kNibHi = 0x00f000f0u;
-// p may grow to this before its reference moves: 2^8 times s^v below 2^7 is in fp16
-constexpr float kKv4Over = 256.f;
-constexpr float kNoRef = 3.4028234e38f;   // minus the reference before the first score: any score then is over
 
 // Keys of a 16-key tile at mma index g (and, 4 further, g + 8) of the score
 // product.  It follows from the second product, whose operand ldmatrix brings
@@ -215,13 +246,15 @@ struct Kv4Row {
 
 // What a warp has of an item: O^T in mma fragments ([m][nt][mma row g8 / g8 + 8],
 // query rows 2 t4 + {0, 1}), the sums of p s^v z likewise (mma rows 0 .. 7 alike,
-// for the even channels, and 8 .. 15), the lane's sums of p, minus the reference (kNoRef: none), the exponent that O
-// and za are scaled by.
+// for the even channels, and 8 .. 15), the lane's sums of p, minus the reference
+// (kNoRef: none), the exponent that O and za are scaled by, with a power of each
+// row's own besides where `wide` is set (OFF_ROWS).
 template <int D, int NT>
 struct Kv4Acc {
     float2 o[D / 16][NT][2], za[NT][2];
     float2 l[NT], nm[NT];
     uint32_t ev;                    // biased exponent of the largest V scale
+    bool wide;
 };
 
 // One warp's attention over `count` key tiles (from tile `first` on) of kv head
@@ -357,7 +390,10 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
     }
     uint32_t& ev = acc.ev;
     ev = 6;
-    float vnorm = __uint_as_float((260u - 6u) << 23);       // 2^(6 - (ev - 127))
+    uint32_t low = 0xffffu;         // the smallest V word so far
+    bool& wide = acc.wide;
+    wide = false;
+    Kv4RowScale* rows = reinterpret_cast<Kv4RowScale*>(ring + C::OFF_ROWS) + 2 * t4;    // of this lane's rows
 
     for (int i = 0; i < count; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_k, phase, wc))) return false;
@@ -365,39 +401,65 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         const int k0 = (first + i) * C::BN;
 
         // ---- scales and zeros: a key a lane
-        const bool edge = k0 + C::BN > nk;
+        const bool masked = k0 + C::BN > nk || (p.causal && k0 + C::BN - 1 > qp_first) ||
+                            (p.window > 0 && k0 <= qp_last - p.window);
         {
             const uint16_t* ws = reinterpret_cast<const uint16_t*>(ring + C::OFF_WORDS);
-            uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0;
+            uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0, bot = 0xffffu;
 #pragma unroll
             for (int kk = 0; kk < C::BN / 32; ++kk) {
                 wk[kk] = ws[kk * 32 + lane];
                 wv[kk] = ws[C::BN + kk * 32 + lane];
-                top = max(top, wv[kk]);
+                if (masked) {       // rows that no query sees may hold anything
+                    const int key = k0 + kk * 32 + lane;
+                    if (key >= nk || (p.causal && key > qp_last) || (p.window > 0 && key <= qp_first - p.window))
+                        wv[kk] = kKv4Unseen;
+                }
+                if (wv[kk] != kKv4Unseen) {
+                    top = max(top, wv[kk]);
+                    bot = min(bot, wv[kk]);
+                }
             }
-            top = __reduce_max_sync(0xffffffffu, top) >> 7;
-            if (edge || top >= 255u) {
-                // rows past the sequence may hold anything; a row whose V is
-                // NaN acts through its score
+            if (__any_sync(0xffffffffu, top >= (ev + 1) << 7 || bot < low)) {
+                // a larger or a smaller scale than any before, or a NaN
                 top = 0;
+                bot = low;
 #pragma unroll
                 for (int kk = 0; kk < C::BN / 32; ++kk) {
-                    if (wv[kk] >= 0x7f80u) {
+                    if (wv[kk] == kKv4Unseen) continue;
+                    if (wv[kk] >= 0x7f80u) {        // acts through the row's score
                         wk[kk] = kKv4NaN;
-                        wv[kk] = 0;
+                        wv[kk] = kKv4Unseen;
+                        continue;
                     }
-                    if (k0 + kk * 32 + lane >= nk) wv[kk] = 0;
                     top = max(top, wv[kk]);
+                    bot = min(bot, wv[kk]);
                 }
                 top = __reduce_max_sync(0xffffffffu, top) >> 7;
-            }
-            if (top > ev) {         // a larger scale than any before: O goes down with the new factor
-                const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
+                low = __reduce_min_sync(0xffffffffu, bot);
+                if (!wide && static_cast<int>(max(top, ev)) - static_cast<int>(low >> 7) > kKv4Spread) {
+                    // from here on a power for each row; its largest w so far, if
+                    // it has met a key, is about that of the largest scale
+                    wide = true;
+                    if (g8 == 0) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) scale_rows(nt, make_float2(d, d));
-                ev = top;
-                vnorm = __uint_as_float((260u - ev) << 23);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float w = ldexpf(1.f, static_cast<int>(ev) - 135);
+                            const int k = 141 - static_cast<int>(ev);
+                            rows[nt * 8] = {w, nm[nt].x, k};
+                            rows[nt * 8 + 1] = {w, nm[nt].y, k};
+                        }
+                    }
+                    ev = 141;           // units of 2^8
+                }
+                if (!wide && top > ev) {        // O goes down with the new factor
+                    const float d = __uint_as_float((127u - min(top - ev, 127u)) << 23);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) scale_rows(nt, make_float2(d, d));
+                    ev = top;
+                }
             }
+            const float vnorm = __uint_as_float((260u - ev) << 23);     // 2^(6 - (ev - 127))
 #pragma unroll
             for (int kk = 0; kk < C::BN / 32; ++kk) {
                 sck[kk * 32 + lane] = make_float2(__uint_as_float((wk[kk] & 0xfff0u) << 16),
@@ -457,7 +519,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
                         s[m][nt][half] = fmul2(ffma2(make_float2(sz.y, sz.y), sq[nt], s[m][nt][half]),
                                                make_float2(sz.x, sz.x));
                 }
-            if (edge || (p.causal && k0 + C::BN - 1 > qp_first) || (p.window > 0 && k0 <= qp_last - p.window)) {
+            if (masked) {
 #pragma unroll
                 for (int m = 0; m < C::MT; ++m)
 #pragma unroll
@@ -515,6 +577,49 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         }
         __syncwarp();               // K may be loaded again
         if (i + 1 < count) load_k(i + 1);
+        if (__builtin_expect(wide, 0)) {
+            // ---- each row's power: its largest w to [2^13, 2^14), p takes the power
+            float2 mx[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mx[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float sv = scv[m * 16 + half * 4 + kkey];
+                        mx[nt].x = fmaxf(mx[nt].x, e[m][nt][half].x * sv);
+                        mx[nt].y = fmaxf(mx[nt].y, e[m][nt][half].y * sv);
+                    }
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) {
+                    mx[nt].x = fmaxf(mx[nt].x, __shfl_xor_sync(0xffffffffu, mx[nt].x, o));
+                    mx[nt].y = fmaxf(mx[nt].y, __shfl_xor_sync(0xffffffffu, mx[nt].y, o));
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                Kv4RowScale r[2] = {rows[nt * 8], rows[nt * 8 + 1]};
+                r[0].take(mx[nt].x, nm[nt].x);
+                r[1].take(mx[nt].y, nm[nt].y);
+                const int k[2] = {kv4_row_power(r[0]), kv4_row_power(r[1])};
+                const int up[2] = {k[0] - r[0].k, k[1] - r[1].k};
+                if (__any_sync(0xffffffffu, up[0] != 0 || up[1] != 0)) {      // in two steps, up to 2^+-250
+                    scale_rows(nt, make_float2(kv4_pow2(up[0] / 2), kv4_pow2(up[1] / 2)));
+                    scale_rows(nt, make_float2(kv4_pow2(up[0] - up[0] / 2), kv4_pow2(up[1] - up[1] / 2)));
+                }
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        e[m][nt][half] = fmul2(e[m][nt][half], make_float2(kv4_pow2(k[0]), kv4_pow2(k[1])));
+                __syncwarp();
+                if (g8 == 0) {
+                    rows[nt * 8] = {r[0].largest, r[0].minus_ref, k[0]};
+                    rows[nt * 8 + 1] = {r[1].largest, r[1].minus_ref, k[1]};
+                }
+            }
+        }
         // ---- p s^v as the B fragments of the second product
         uint32_t pf[C::MT][NT][2];
 #pragma unroll
@@ -568,9 +673,9 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
 // lane has channels 16 m + 2 g8 + {0, 1}, m < D / 16, of two rows of each nt.
 // O is left as it is (relative to the reference).
 template <int D, int NT, typename Put>
-__device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, int nrows, const Put& put) {
+__device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, const uint8_t* ring, int nrows, const Put& put) {
     const int t4 = lane_id() & 3;
-    const float back = ldexpf(1.f, static_cast<int>(acc.ev) - 133);       // undoes vnorm
+    const Kv4RowScale* rows = reinterpret_cast<const Kv4RowScale*>(ring + Kv4DecCfg<D, NT>::OFF_ROWS);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -582,6 +687,8 @@ __device__ __forceinline__ void kv4_each_row(Kv4Acc<D, NT>& acc, int nrows, cons
         for (int j = 0; j < 2; ++j) {
             const int r = nt * 8 + 2 * t4 + j;
             if (r >= nrows) continue;
+            // undoes vnorm, and the row's power
+            const float back = ldexpf(1.f, static_cast<int>(acc.ev) - 133 - (acc.wide ? rows[r].k : 0));
             const float z0 = j ? acc.za[nt][0].y : acc.za[nt][0].x, z1 = j ? acc.za[nt][1].y : acc.za[nt][1].x;
             const float n1 = j ? acc.nm[nt].y : acc.nm[nt].x;
             float a[D / 8];
@@ -666,7 +773,7 @@ kv4_cluster_kernel(const __grid_constant__ CUtensorMap tm_v, const Kv4DecodePara
     if (!ok) kv4_drain(bar_k, phase, p.error_word);
     auto partial = [&](int w) { return reinterpret_cast<float*>(smem + w * C::WARP_BYTES); };   // [ROWS][OSTRIDE]
     auto stats = [&](int w) { return partial(w) + C::ROWS * C::OSTRIDE; };                      // [ROWS][2]
-    kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
+    kv4_each_row<D, NT>(acc, smem + warp * C::WARP_BYTES, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
         float2* dst = reinterpret_cast<float2*>(partial(warp) + r * C::OSTRIDE + 2 * g8);
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) dst[8 * m] = make_float2(a[2 * m], a[2 * m + 1]);
@@ -831,7 +938,7 @@ kv4_decode_kernel(const __grid_constant__ CUtensorMap tm_v, const Kv4DecodeParam
             return;
         }
         const bool whole = count == sp.n;
-        kv4_each_row<D, NT>(acc, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
+        kv4_each_row<D, NT>(acc, smem + warp * C::WARP_BYTES, nrows, [&](int r, const float (&a)[D / 8], float ref, float l) {
             if (whole) {
                 const bool some = !(l == 0.f);      // a NaN sum stays NaN
                 const float inv = some ? 1.f / l : 0.f;

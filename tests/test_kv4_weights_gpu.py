@@ -131,3 +131,94 @@ def test_equal_weights_of_rows_near_their_zero(d, num_splits):
         q = torch.zeros((1, 1, 4, d), dtype=torch.bfloat16, device=DEV)
         q[..., 0] = torch.tensor([1.0, 2.0, 3.0, 5.0], device=DEV)
         check(q, cache, full([n]), True, 0, num_splits)
+
+
+UPS = [12, 20, 24, 31, 40, 64, 100, 120]
+
+
+def raise_row(cache, at, up, b=0, hk=0):
+    """V row `at` 2^up times as large, half of that by making the others smaller."""
+    down = up // 2
+    cache["v_words"] -= down << 7
+    cache["v_words"][b, hk, at] += up << 7
+    return cache
+
+
+@pytest.mark.parametrize("up", UPS)
+@pytest.mark.parametrize("B,Nq,H,Hkv,Nk,d", [(1, 2, 1, 1, 64, 128), (1, 4, 8, 2, 520, 128), (1, 3, 2, 2, 712, 64),
+                                            (1, 16, 2, 1, 2048, 128)])
+@pytest.mark.parametrize("num_splits", [0, 1, 3])
+def test_a_large_row_that_a_mask_hides(up, B, Nq, H, Hkv, Nk, d, num_splits):
+    # the last key is seen by the last query alone; the first key by the first
+    # queries under a window
+    q = queries(B, Nq, H, d, 5)
+    check(q, raise_row(random_cache(B, Nk, Hkv, d, 8), Nk - 1, up), full([Nk]), True, 0, num_splits)
+    window = min(Nk // 2, 40)
+    at = Nk - Nq - window + 1         # the first key of query 0, before all others' windows
+    check(q, raise_row(random_cache(B, Nk, Hkv, d, 9), at, up), full([Nk]), True, window, num_splits)
+    if at > 0:                        # and one that no query sees, in a tile that they read
+        check(q, raise_row(random_cache(B, Nk, Hkv, d, 9), at - 1, up), full([Nk]), True, window, num_splits)
+
+
+@pytest.mark.parametrize("up", UPS)
+@pytest.mark.parametrize("at", [0, 70, 511])
+@pytest.mark.parametrize("low", [8.0, 20.0, 45.0, 70.0])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_a_large_row_of_little_weight(up, at, low, num_splits):
+    # one V row 2^up times the others, its key's weight 2^-low of theirs: either
+    # may decide the result
+    d, n = 128, 512
+    g = torch.Generator("cpu").manual_seed(17)
+    q = torch.randn((1, 1, 1, d), generator=g).to(torch.bfloat16)
+    k = torch.randn((1, n, 1, d), generator=g) * 0.1
+    k[0, at, 0] = -q[0, 0, 0].float() * (low * math.log(2.0) * d ** 0.5 / q.float().pow(2).sum())
+    v = torch.randn((1, n, 1, d), generator=g) * 2.0 ** (-(up // 2))
+    v[0, at] *= 2.0 ** up
+    cache = fa.quantize_kv4(k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), fa.kv4_cache(1, n, 1, d))
+    check(q.to(DEV), cache, full([n]), True, 0, num_splits)
+
+
+@pytest.mark.parametrize("zero", [0, 2.0 ** -126])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_a_row_of_zeros_takes_the_weight(zero, d, num_splits):
+    # a key with nearly all the weight whose values are 0: the others' rows make
+    # the result, at 2^-30 of its weight
+    n = 300
+    g = torch.Generator("cpu").manual_seed(18)
+    q = torch.randn((1, 1, 2, d), generator=g).to(torch.bfloat16)
+    q[0, 0, 1] = q[0, 0, 0]
+    k = torch.randn((1, n, 1, d), generator=g) * 0.1
+    k[0, 3, 0] = q[0, 0, 0].float() * (30 * math.log(2.0) * d ** 0.5 / q[0, 0, 0].float().pow(2).sum())
+    v = torch.randn((1, n, 1, d), generator=g)
+    v[0, 3] = 0
+    cache = fa.quantize_kv4(k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), fa.kv4_cache(1, n, 1, d))
+    if zero == 0:
+        cache["v_words"][0, 0, 3] = 0         # as in a cache that nothing was written to
+    check(q.to(DEV), cache, full([n]), True, 0, num_splits)
+
+
+@pytest.mark.parametrize("num_splits", [0, 1])
+@pytest.mark.parametrize("step", [-3, 3])
+def test_scales_that_fall_or_grow_by_tiles(num_splits, step):
+    # each 64-key tile's values 2^step times those of the one before
+    n, d = 1600, 128
+    cache = random_cache(1, n, 1, d, 10)
+    tile = torch.arange(n, device=DEV) // 64
+    cache["v_words"] += ((tile * step - step * 12) << 7).to(torch.int16)
+    check(queries(1, 2, 4, d, 5), cache, full([n]), True, 0, num_splits)
+    check(queries(1, 2, 4, d, 6), cache, full([n]), True, 64, num_splits)
+
+
+def test_the_chunk_path_agrees():
+    # the same rows, few queries on the codes and many read back
+    d, n, up = 128, 520, 31
+    cache = raise_row(random_cache(1, n, 20, d, 8), n - 1, up)
+    cache["v_words"][:, 1:] = cache["v_words"][:, :1]
+    q = queries(1, 250, 40, d, 5)
+    assert not runs_on_the_codes(q, cache, 0, 1)
+    o, _ = fa.forward_kv4(q, cache, causal=True, num_splits=1)
+    few = q[:, -4:].contiguous()
+    O, _, bo = tight_reference(few, cache, [n], True, 0, d ** -0.5)
+    got, _ = check(few, cache, full([n]), True, 0, 1)
+    assert ((o[:, -4:-1].double() - O[:, :-1]).abs() <= 8 * bo[:, :-1] + 2.0 ** -6 * O[:, :-1].abs().amax(-1, True)).all()
