@@ -353,8 +353,10 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -5.9604644775390625e-8f;                                // -2^-24, as the codes
-        const float f = e >= 255 ? NAN : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
+        // a query with NaN or infinity has NaN scores (through its sum; the factor
+        // stays finite), which the masks replace: without a key it has O = 0
+        sum = e >= 255 ? NAN : sum * -5.9604644775390625e-8f;          // -2^-24, as the codes
+        const float f = e >= 255 ? 1.f : ldexpf(p.scale_log2, e - 117);    // / (qs 2^-24)
         sq[nt].x = __shfl_sync(0xffffffffu, sum, 8 * t4);
         sq[nt].y = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
         rf[nt].x = __shfl_sync(0xffffffffu, f, 8 * t4);

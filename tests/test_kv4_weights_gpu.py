@@ -222,3 +222,27 @@ def test_the_chunk_path_agrees():
     O, _, bo = tight_reference(few, cache, [n], True, 0, d ** -0.5)
     got, _ = check(few, cache, full([n]), True, 0, 1)
     assert ((o[:, -4:-1].double() - O[:, :-1]).abs() <= 8 * bo[:, :-1] + 2.0 ** -6 * O[:, :-1].abs().amax(-1, True)).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("Nq,H,Hkv", [(4, 2, 1), (12, 4, 2), (250, 40, 20)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_a_nan_query_without_a_key(bad, Nq, H, Hkv, d, num_splits):
+    # queries before the first key give O = 0 and LSE = -inf whatever they hold
+    cache = random_cache(3, 304, Hkv, d, 19)
+    lens = torch.tensor([2, 0, Nq - 1], dtype=torch.int32, device=DEV)
+    q = queries(3, Nq, H, d, 20)
+    clean, clean_lse = fa.forward_kv4(q, cache, lens, causal=True, num_splits=num_splits)
+    for b, n in enumerate(lens.tolist()):
+        q[b, :Nq - n, :, 3] = bad
+    o, lse = fa.forward_kv4(q, cache, lens, causal=True, num_splits=num_splits)
+    assert torch.equal(o, clean) and torch.equal(lse, clean_lse)
+    for b, n in enumerate(lens.tolist()):
+        assert torch.count_nonzero(o[b, :Nq - n]) == 0 and torch.isneginf(lse[b, :, :Nq - n]).all()
+    # and one with keys makes its own row NaN alone
+    q[0, Nq - 1, 0, 3] = bad
+    o, _ = fa.forward_kv4(q, cache, lens, causal=True, num_splits=num_splits)
+    assert torch.isnan(o[0, Nq - 1, 0]).all()
+    o[0, Nq - 1, 0] = clean[0, Nq - 1, 0]
+    assert torch.equal(o, clean)
