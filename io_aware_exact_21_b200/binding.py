@@ -122,6 +122,28 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _alloc(stream, make, output=True):
+    """make(), a tensor, allocated and filled on the stream that the call runs on:
+    there the fill comes before the call's kernels, and a workspace that is
+    dropped when the call returns goes to no other stream while they use it.  An
+    output is also marked as in use by the current stream, where the caller will
+    read it (once ordered after `stream`)."""
+    if stream is None:
+        return make()
+    torch = _torch()
+    current = torch.cuda.current_stream()
+    handle = _stream(stream)
+    if handle == current.cuda_stream:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):       # (0 as an external stream would make a new one)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = make()
+    if output:
+        t.record_stream(current)
+    return t
+
+
 def _check(code: int, where: str):
     if code != FA_OK:
         raise FaError(code, where)
@@ -289,6 +311,10 @@ def fa_profile_end():
 # that does not match them (dtype, shape, contiguity, device), so that a
 # mismatch raises here instead of making a kernel touch memory outside a
 # tensor.  The raw fa_* functions above take pointers and do no such check.
+#
+# stream (a torch stream or a handle; None: the current one) is where a call runs.
+# What a wrapper allocates belongs to that stream (_alloc); the order between the
+# streams that make the inputs, run the call and read the results is the caller's.
 
 def _require_cuda(t, name):
     if not t.is_cuda:
@@ -352,9 +378,9 @@ def forward(q, k, v, causal=False, window=0, cu_seqlens=None, scale=None, out=No
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, lambda: torch.empty_like(q))
     if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+        lse = _alloc(stream, lambda: torch.empty(lse_shape, dtype=torch.float32, device=dev))
     _expect(out, "out", q.shape, torch.bfloat16, dev)
     _expect(lse, "lse", lse_shape, torch.float32, dev)
     _check(fa_fwd(q, k, v, out, lse, B, H, N, d, scale, causal, window, cu_seqlens, stream),
@@ -389,9 +415,9 @@ def forward_kv(q, k, v, causal=False, window=0, cu_seqlens_q=None, cu_seqlens_k=
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, lambda: torch.empty_like(q))
     if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+        lse = _alloc(stream, lambda: torch.empty(lse_shape, dtype=torch.float32, device=dev))
     _expect(out, "out", q.shape, torch.bfloat16, dev)
     _expect(lse, "lse", lse_shape, torch.float32, dev)
     _check(fa_fwd_kv(q, k, v, out, lse, B, H, Nq, Nk, d, scale, causal, window, cu_seqlens_q,
@@ -419,15 +445,15 @@ def forward_kvcache(q, k_cache, v_cache, seqlens_k=None, causal=False, window=0,
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, lambda: torch.empty_like(q))
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+        lse = _alloc(stream, lambda: torch.empty((B, H, Nq), dtype=torch.float32, device=dev))
     _expect(out, "out", q.shape, torch.bfloat16, dev)
     _expect(lse, "lse", (B, H, Nq), torch.float32, dev)
     ns = num_splits if num_splits > 0 else fa_fwd_kvcache_num_splits(B, H, Nq, Nk, d)
     need = fa_fwd_kvcache_workspace_size(B, H, Nq, d, ns)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _alloc(stream, lambda: torch.empty(need, dtype=torch.uint8, device=dev), output=False)
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, dev)
     _check(fa_fwd_kvcache(q, k_cache, v_cache, out, lse, B, H, Nq, Nk, d, scale, causal, window,
@@ -571,7 +597,9 @@ def dequantize_kv4(cache, rows=None, starts=None, lens=None, cu_seqlens=None, ou
                 raise ValueError("a packed read needs rows or out")
             rows = Nk
         shape = (B, rows, Hkv, 2 * half) if cu_seqlens is None else (rows, Hkv, 2 * half)
-        out = tuple(torch.zeros(shape, dtype=torch.bfloat16, device=cache["k_codes"].device)
+        dev = cache["k_codes"].device
+        _expect_kv4_cache(cache, B, Hkv, 2 * half, dev)
+        out = tuple(_alloc(stream, lambda: torch.zeros(shape, dtype=torch.bfloat16, device=dev))
                     for _ in range(2))
     k, v = out
     kc, kw, vc, vw, B, N, Hkv, Nk, d = _kv4_rows(k, v, cache, cu_seqlens, starts, lens)
@@ -612,11 +640,11 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _alloc(stream, lambda: torch.empty_like(q))
     else:
         _expect(out, "out", shape, torch.bfloat16, q.device)
     if lse is None:
-        lse = q.new_empty((B, H, Nq), dtype=torch.float32)
+        lse = _alloc(stream, lambda: q.new_empty((B, H, Nq), dtype=torch.float32))
     else:
         _expect(lse, "lse", (B, H, Nq), torch.float32, q.device)
     lib = load_library()
@@ -625,7 +653,7 @@ def forward_kv4(q, cache, seqlens_k=None, causal=False, window=0, scale=None, nu
     if workspace is not None:
         _expect_bytes(workspace, "workspace", need, q.device)
     elif need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = _alloc(stream, lambda: q.new_empty(need, dtype=torch.uint8), output=False)
     _check(lib.fa_fwd_kv4(
         q.data_ptr(), kc.data_ptr(), kw.data_ptr(), vc.data_ptr(), vw.data_ptr(), out.data_ptr(),
         lse.data_ptr(), B, H, Hkv, Nq, Nk, d, float(scale), int(causal), window, _ptr(seqlens_k), num_splits,
@@ -647,12 +675,12 @@ def quantize_fp8(q, k, v, signs=None, stream=None):
         _expect(t, name, q.shape, torch.bfloat16, dev)
     if signs is not None:
         _expect(signs, "signs", (d,), torch.float32, dev)
-    out = {"q8": torch.empty((B, N, H, d), dtype=torch.uint8, device=dev),
-           "k8": torch.empty((B, N, H, d), dtype=torch.uint8, device=dev),
-           "vt8": torch.empty(max(1, fa_fp8_vt_bytes(B, H, N, d)), dtype=torch.uint8, device=dev),
-           "sq": torch.empty((B, H, nb), dtype=torch.float32, device=dev),
-           "sk": torch.empty((B, H, nb), dtype=torch.float32, device=dev),
-           "sv": torch.empty((B, H, nb), dtype=torch.float32, device=dev)}
+    def empty(shape, dtype):
+        return _alloc(stream, lambda: torch.empty(shape, dtype=dtype, device=dev))
+    out = {"q8": empty((B, N, H, d), torch.uint8), "k8": empty((B, N, H, d), torch.uint8),
+           "vt8": empty(max(1, fa_fp8_vt_bytes(B, H, N, d)), torch.uint8),
+           "sq": empty((B, H, nb), torch.float32), "sk": empty((B, H, nb), torch.float32),
+           "sv": empty((B, H, nb), torch.float32)}
     _check(fa_quantize_fp8(q, out["q8"], out["sq"], B, N, H, d, 0, signs, stream), "fa_quantize_fp8")
     _check(fa_quantize_fp8(k, out["k8"], out["sk"], B, N, H, d, 0, signs, stream), "fa_quantize_fp8")
     _check(fa_quantize_fp8(v, out["vt8"], out["sv"], B, N, H, d, 1, None, stream), "fa_quantize_fp8")
@@ -673,9 +701,9 @@ def forward_fp8(qz, B, N, H, d=128, causal=False, window=0, scale=None, out=None
     for name in ("sq", "sk", "sv"):
         _expect(qz[name], name, (B, H, nb), torch.float32, dev)
     if out is None:
-        out = torch.empty((B, N, H, d), dtype=torch.bfloat16, device=dev)
+        out = _alloc(stream, lambda: torch.empty((B, N, H, d), dtype=torch.bfloat16, device=dev))
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+        lse = _alloc(stream, lambda: torch.empty((B, H, N), dtype=torch.float32, device=dev))
     _expect(out, "out", (B, N, H, d), torch.bfloat16, dev)
     _expect(lse, "lse", (B, H, N), torch.float32, dev)
     _check(fa_fwd_fp8(qz["q8"], qz["k8"], qz["vt8"], qz["sq"], qz["sk"], qz["sv"], out, lse, B, H,
@@ -698,14 +726,14 @@ def backward(q, k, v, o, lse, dout, causal=False, window=0, cu_seqlens=None, sca
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+        grads = tuple(_alloc(stream, lambda: torch.empty_like(q)) for _ in range(3))
     dq, dk, dv = grads
     for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
         _expect(t, name, q.shape, torch.bfloat16, dev)
     size_fn = fa_bwd_fused_workspace_size if fused else fa_bwd_workspace_size
     ws_bytes = size_fn(B, H, N, d, N if cu_seqlens is not None else 0)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _alloc(stream, lambda: torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev), output=False)
     _expect_bytes(workspace, "workspace", ws_bytes, dev)
     fn = fa_bwd_fused if fused else fa_bwd
     _check(fn(q, k, v, o, lse, dout, dq, dk, dv, B, H, N, d, scale, causal, window,
