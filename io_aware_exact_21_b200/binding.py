@@ -113,10 +113,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        # the handle alone: torch.cuda.current_stream() makes a Stream object
-        # around it, which costs as much as the rest of a small call's checks
-        c = _torch()._C
-        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        return _torch().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
