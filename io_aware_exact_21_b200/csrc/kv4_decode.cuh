@@ -68,6 +68,7 @@
 
 #include "decode_kernel.cuh"
 #include "kv4_rows.cuh"
+#include "kv4_span.cuh"
 
 namespace fa {
 
@@ -199,9 +200,8 @@ template <int BN>
 __device__ __forceinline__ Kv4Span kv4_span(const Kv4DecodeParams& p, int b) {
     Kv4Span s;
     s.nk = p.seqlens_k ? min(max(p.seqlens_k[b], 0), p.Nk) : p.Nk;
-    const int64_t first = static_cast<int64_t>(s.nk) - p.Nq - p.window + 1;
-    s.t0 = p.window > 0 && first > 0 ? static_cast<int>(first) / BN : 0;
-    s.n = (s.nk + BN - 1) / BN - s.t0;
+    s.t0 = kv4_first_tile(s.nk, p.Nq, p.window, BN);
+    s.n = kv4_tile_count(s.nk, BN) - s.t0;
     return s;
 }
 
@@ -363,9 +363,9 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         rf[nt].y = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int qp = qpos0 + (r0 + nt * 8 + 2 * t4 + j) / p.G;
-            hi[nt][j] = p.causal ? min(nk, qp + 1) : nk;
-            lo[nt][j] = p.window > 0 ? max(0, qp - p.window + 1) : 0;
+            const int qp = qpos0 + (r0 + min(nt * 8 + 2 * t4 + j, nrows - 1)) / p.G;
+            hi[nt][j] = kv4_key_hi(qp, nk, p.causal);
+            lo[nt][j] = kv4_key_lo(qp, p.window);
         }
     }
     const int qp_first = qpos0 + r0 / p.G, qp_last = qpos0 + (r0 + nrows - 1) / p.G;
@@ -403,8 +403,7 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
         const int k0 = (first + i) * C::BN;
 
         // ---- scales and zeros: a key a lane
-        const bool masked = k0 + C::BN > nk || (p.causal && k0 + C::BN - 1 > qp_first) ||
-                            (p.window > 0 && k0 <= qp_last - p.window);
+        const bool masked = kv4_tile_masked(k0, C::BN, nk, qp_first, qp_last, p.causal, p.window);
         {
             const uint16_t* ws = reinterpret_cast<const uint16_t*>(ring + C::OFF_WORDS);
             uint32_t wk[C::BN / 32], wv[C::BN / 32], top = 0, bot = 0xffffu;
@@ -412,11 +411,9 @@ __device__ __forceinline__ bool kv4_attend(const Kv4DecodeParams& p, const CUten
             for (int kk = 0; kk < C::BN / 32; ++kk) {
                 wk[kk] = ws[kk * 32 + lane];
                 wv[kk] = ws[C::BN + kk * 32 + lane];
-                if (masked) {       // rows that no query sees may hold anything
-                    const int key = k0 + kk * 32 + lane;
-                    if (key >= nk || (p.causal && key > qp_last) || (p.window > 0 && key <= qp_first - p.window))
-                        wv[kk] = kKv4Unseen;
-                }
+                // rows that no query sees may hold anything
+                if (masked && kv4_unseen(k0 + kk * 32 + lane, nk, qp_first, qp_last, p.causal, p.window))
+                    wv[kk] = kKv4Unseen;
                 if (wv[kk] != kKv4Unseen) {
                     top = max(top, wv[kk]);
                     bot = min(bot, wv[kk]);
