@@ -113,7 +113,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        # 0.6 us; torch.cuda.current_stream() makes a Stream object in Python, 3.2 us
+        torch = _torch()
+        return torch.accelerator.current_stream(torch.cuda.current_device()).native_handle
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -128,10 +130,10 @@ def _alloc(stream, make, output=True):
     if stream is None:
         return make()
     torch = _torch()
-    current = torch.cuda.current_stream()
     handle = _stream(stream)
-    if handle == current.cuda_stream:
+    if handle == _stream(None):
         return make()
+    current = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):       # (0 as an external stream would make a new one)
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     with torch.cuda.stream(stream):

@@ -9,11 +9,14 @@ from io_aware_exact_21_b200 import binding as bd
 
 class Fake:
     cuda_stream = 0x1234
+    native_handle = 0x5678
 
 
 def test_the_current_stream_is_the_public_one(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Fake())
-    assert bd._stream(None) == 0x1234
+    # of the current device
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.accelerator, "current_stream", lambda device=None: Fake() if device == 3 else None)
+    assert bd._stream(None) == 0x5678
 
 
 def test_a_given_stream():
