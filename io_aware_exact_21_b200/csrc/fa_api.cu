@@ -437,7 +437,7 @@ int launch_chunk(const void* q, const void* k_cache, const void* v_cache, void* 
     const int64_t rows_q = static_cast<int64_t>(B) * Nq;
     const int64_t rows_k = static_cast<int64_t>(B) * Nk;
     const int Hk = H / group;
-    if (rows_q > (int64_t{1} << 31) - 1) return FA_ERR_BAD_SHAPE;
+    if (rows_q > (int64_t{1} << 31) - 1 || (ns > 1 && rows_q * H > fa::kMaxGridWarps)) return FA_ERR_BAD_SHAPE;
     // with no cache rows at all the maps are pointed at q: every key tile is
     // then read at rows [-128, 0), outside the map, so nothing of q is read
     const void* kk = rows_k > 0 ? k_cache : q;
@@ -613,7 +613,8 @@ bool kv4_bad_attention(int B, int H, int Hkv, int Nq, int Nk, int d, int window,
     const int64_t rows_q = static_cast<int64_t>(B) * Nq, rows = static_cast<int64_t>(Nq) * (H / Hkv);
     if (rows_q > kMax || rows_q * H > (int64_t{1} << 40) / d || rows > kMax) return true;
     if (rows_q == 0) return false;
-    if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms)) return H / Hkv > 65535;
+    if (!kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms))
+        return H / Hkv > 65535 || rows_q * H > fa::kMaxGridWarps;
     return rows_q * H > kMax ||      // a CTA each in the merge; the key tiles are counted in 32 bits
            static_cast<int64_t>(B) * Hkv * (Nk / 32 + 2) * kv4_row_blocks(rows) > kMax;
 }

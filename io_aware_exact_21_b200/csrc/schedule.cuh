@@ -53,6 +53,13 @@ struct SeqSpan {
     int len;
 };
 
+// Warp of the grid, for kernels with a warp to each (row, head): warps are counted
+// in 32 bits (kMaxGridWarps), threads would pass them at 2^27 warps.
+constexpr int64_t kMaxGridWarps = (int64_t{1} << 32) - 1;
+__device__ __forceinline__ uint32_t grid_warp() {
+    return blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+}
+
 // Allowed-key test for one (row, key) pair inside a sequence.
 __device__ __forceinline__ bool key_allowed(int i, int j, int n, int causal, int window) {
     return j < n && (!causal || j <= i) && (window <= 0 || j > i - window);
