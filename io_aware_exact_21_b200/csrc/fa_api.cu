@@ -653,7 +653,7 @@ int kv4_rows(const void* k, const void* v, const void* k_codes, const void* k_wo
     if (N < 0 || kv4_bad_cache(B, Hkv, Nk, d)) return FA_ERR_BAD_SHAPE;
     if (cu_seqlens && (lens || B > fa::kMaxVarlenSeqs)) return FA_ERR_BAD_SHAPE;
     const int64_t rows = cu_seqlens ? static_cast<int64_t>(N) : static_cast<int64_t>(B) * N;
-    if (rows > (int64_t{1} << 31) - 1 || rows * Hkv * d > (int64_t{1} << 40)) return FA_ERR_BAD_SHAPE;
+    if (rows > (int64_t{1} << 31) - 1 || rows * Hkv > (int64_t{1} << 40) / d) return FA_ERR_BAD_SHAPE;
     const int64_t rows_k = static_cast<int64_t>(B) * Nk;
     if (rows > 0 && (!k || !v)) return FA_ERR_NULLPTR;
     if (rows_k > 0 && (!k_codes || !k_words || !v_codes || !v_words)) return FA_ERR_NULLPTR;
