@@ -446,11 +446,11 @@ combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_p
     // launched as a programmatic dependent of the split kernel: wait until it
     // has completed and its partials are visible (returns at once otherwise)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint32_t warp = grid_warp();
+    const int warp_global = grid_warp();
     const int lane = lane_id();
-    if (warp >= static_cast<uint64_t>(rows) * H) return;
-    const int row = static_cast<int>(warp / static_cast<uint32_t>(H));
-    const int h = static_cast<int>(warp - static_cast<uint32_t>(row) * H);
+    if (warp_global >= rows * H) return;
+    const int row = warp_global / H;
+    const int h = warp_global - row * H;
     const float l2 = lane < nsplit ? lse_part[(static_cast<size_t>(lane) * H + h) * rows + row]
                                    : -INFINITY;
     float M = l2;

@@ -55,9 +55,9 @@ struct SeqSpan {
 
 // Warp of the grid, for kernels with a warp to each (row, head): warps are counted
 // in 32 bits (kMaxGridWarps), threads would pass them at 2^27 warps.
-constexpr int64_t kMaxGridWarps = (int64_t{1} << 32) - 1;
-__device__ __forceinline__ uint32_t grid_warp() {
-    return blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+constexpr int64_t kMaxGridWarps = (int64_t{1} << 31) - 8;
+__device__ __forceinline__ int grid_warp() {
+    return static_cast<int>(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
 }
 
 // Allowed-key test for one (row, key) pair inside a sequence.

@@ -22,7 +22,7 @@ static inline void __syncthreads() {}
 int main() {
     blockDim.x = 256;
     const int64_t last = fa::kMaxGridWarps / 8;
-    const int64_t from[] = {0, (int64_t{1} << 24) - 3, (int64_t{1} << 27) - 3, (int64_t{1} << 28) - 3, last - 6};
+    const int64_t from[] = {0, (int64_t{1} << 24) - 3, (int64_t{1} << 27) - 3, (int64_t{1} << 27) + 12345, last - 6};
     for (int64_t f : from)
         for (int64_t b = f; b < f + 6; ++b)
             for (unsigned t = 0; t < 256; ++t) {
