@@ -235,7 +235,8 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  *   Few query rows to a key/value head (Nq * H / Hkv up to about 100, more where
  * the whole problem is small) run on kernels that multiply the 4-bit codes as
  * they are; more are run by reading the rows in use back into the workspace for
- * the tensor-core forward.
+ * the tensor-core forward: K and V in bf16, 4 d bytes a row and head, for Nk rows
+ * a sequence, or for the window + Nq + 126 that a window leaves where that is less.
  *   num_splits : few rows: the keys of all sequences and heads together are
  * cut into equal ranges, num_splits to each (sequence, key/value head) on
  * average; chunks: as fa_fwd_kvcache.  0 lets the library choose; at most 32.

@@ -562,11 +562,21 @@ int current_sms() {
     return sms > 0 ? sms : 148;
 }
 
-// Bytes of the bf16 K (and of the V) that a chunk is read back into.
-size_t kv4_readback_bytes(int B, int Hkv, int Nk, int d) {
-    const size_t bytes = static_cast<size_t>(B) * Nk * Hkv * d * 2;
-    return (bytes + 255) & ~static_cast<size_t>(255);
+size_t up_256(size_t bytes) { return (bytes + 255) & ~static_cast<size_t>(255); }
+
+// Rows of a sequence that a chunk is read back into: all that it has room for, or
+// those that the queries read under a window, from the start of a 128-key tile on.
+int kv4_back_rows(int Nq, int Nk, int window) {
+    return window > 0 ? static_cast<int>(std::min<int64_t>(Nk, static_cast<int64_t>(window) + Nq + 126)) : Nk;
 }
+
+// Bytes of the bf16 K (and of the V) that a chunk is read back into.
+size_t kv4_readback_bytes(int B, int Hkv, int rows, int d) {
+    return up_256(static_cast<size_t>(B) * rows * Hkv * d * 2);
+}
+
+// Bytes of the lengths that go with it under a window.
+size_t kv4_back_lens_bytes(int B, int window) { return window > 0 ? up_256(static_cast<size_t>(B) * 4) : 0; }
 
 // Ranges that a chunk's keys are cut into: as many as the SMs hold blocks of 256
 // rows at once, never more (a second round of blocks costs as much as the first),
@@ -595,9 +605,12 @@ size_t kv4_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, 
     return (rows * (static_cast<size_t>(d) + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
 
+// (a window as wide as the cache is none)
 size_t kv4_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int num_splits, int num_sms) {
+    if (window >= Nk) window = 0;
     const size_t part = kv4_part_bytes(B, H, Hkv, Nq, Nk, d, window, num_splits, num_sms);
-    return kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms) ? part : part + 2 * kv4_readback_bytes(B, Hkv, Nk, d);
+    if (kv4_direct(B, Hkv, Nq, H / Hkv, Nk, window, num_sms)) return part;
+    return part + kv4_back_lens_bytes(B, window) + 2 * kv4_readback_bytes(B, Hkv, kv4_back_rows(Nq, Nk, window), d);
 }
 
 bool kv4_bad_cache(int B, int Hkv, int Nk, int d) {
@@ -1009,18 +1022,22 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         // read the rows in use back into the workspace (exactly: they are bf16
         // numbers) and run the chunk on the tensor-core forward
         const int ns = num_splits > 0 ? num_splits : kv4_chunk_splits(B, H, Hkv, Nq, Nk, window, num_sms);
+        const int back_rows = kv4_back_rows(Nq, Nk, window);
         uint8_t* back = static_cast<uint8_t*>(workspace) + decode_workspace_bytes(B, H, Nq, d, ns);
+        int* back_lens = window > 0 ? reinterpret_cast<int*>(back) : nullptr;
+        back += kv4_back_lens_bytes(B, window);
         void* kb = back;
-        void* vb = back + kv4_readback_bytes(B, Hkv, Nk, d);
+        void* vb = back + kv4_readback_bytes(B, Hkv, back_rows, d);
         fa::Kv4Params r = {};
         r.place.lens = seqlens_k;
         r.place.B = B;
-        r.place.N = Nk;
+        r.place.N = back_rows;
         r.place.H = Hkv;
         r.place.Nk = Nk;
         r.place.from_window = window > 0 ? window : 0;
         r.place.from_queries = Nq;
-        r.rows = rows_k;
+        r.rows = static_cast<int64_t>(B) * back_rows;
+        r.back_lens = back_lens;
         r.x[0] = static_cast<__nv_bfloat16*>(kb);
         r.x[1] = static_cast<__nv_bfloat16*>(vb);
         r.codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
@@ -1031,8 +1048,8 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_words, const vo
         rc = d == 64 ? launch_kv4_rows<64, false>(r, st->num_sms, stream)
                      : launch_kv4_rows<128, false>(r, st->num_sms, stream);
         if (rc != FA_OK) return rc;
-        return launch_chunk(q, kb, vb, o, lse, B, H, group, Nq, Nk, d, scale, causal, window, seqlens_k, ns,
-                            part, st, stream);
+        return launch_chunk(q, kb, vb, o, lse, B, H, group, Nq, back_rows, d, scale, causal, window,
+                            window > 0 ? back_lens : seqlens_k, ns, part, st, stream);
     }
 
     fa::Kv4DecodeParams p;

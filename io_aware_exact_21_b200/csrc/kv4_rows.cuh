@@ -37,18 +37,21 @@ struct Kv4Place {
     const int* lens;         // or nullptr (all N)
     int B, N, H;             // N: rows a sequence; packed: all rows
     int Nk;                  // cache rows a sequence has room for
-    int from_window;         // > 0: rows of positions that no query of the
-    int from_queries;        //   attention call needs are left out (see first_row)
+    int from_window;         // > 0 (fixed length, no starts): row 0 of the bf16 side is the first
+    int from_queries;        //   that the attention call's queries read (kv4_first_row), N the room there
 };
 
 // For attention under a sliding window: the first cache row that the last
-// `from_queries` positions of a sequence of n rows read, with the 128-key tile
-// that holds it and the last (right-aligned) tile whole.
+// `from_queries` positions of a sequence of n rows read, in whole 128-key tiles.
 __device__ __forceinline__ int kv4_first_row(const Kv4Place& w, int n) {
     if (w.from_window <= 0) return 0;
     const int64_t first = static_cast<int64_t>(n) - w.from_queries - w.from_window + 1;
-    if (first <= 0) return 0;
-    return max(0, min(static_cast<int>(first) / 128 * 128, n - 128));
+    return first > 0 ? static_cast<int>(first) / 128 * 128 : 0;
+}
+
+// The cache rows of sequence b that such a call uses.
+__device__ __forceinline__ int kv4_used(const Kv4Place& w, int b) {
+    return w.lens ? min(max(w.lens[b], 0), w.Nk) : w.Nk;
 }
 
 // Sequence and cache row of row r of the [rows, H, D] side; false when r
@@ -69,8 +72,13 @@ __device__ __forceinline__ bool kv4_place(const Kv4Place& w, int64_t r, int64_t 
     } else {
         b = static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(w.N));   // rows < 2^31
         i = r - static_cast<int64_t>(b) * w.N;
-        const int n = w.lens ? min(w.lens[b], w.N) : w.N;
-        if (i >= n || i < kv4_first_row(w, n)) return false;
+        if (w.from_window > 0) {
+            const int n = kv4_used(w, b);
+            i += kv4_first_row(w, n);
+            if (i >= n) return false;
+        } else if (i >= (w.lens ? min(w.lens[b], w.N) : w.N)) {
+            return false;
+        }
     }
     const int64_t at = (w.starts ? w.starts[b] : 0) + i;
     pos = static_cast<int>(at);
@@ -199,6 +207,7 @@ struct Kv4Params {
     uint8_t* codes[2];             // [B, H, Nk, D / 2]
     uint16_t* words[2];            // [B, H, Nk]
     int poison;                    // reading for attention: see kv4_read_kernel
+    int* back_lens;                // or nullptr: for from_window, the rows read back of each sequence
 };
 
 constexpr int kKv4Warps = 8;
@@ -277,11 +286,20 @@ kv4_write_kernel(const Kv4Params p) {
 
 // Reads cache rows back as bf16.  poison (attention's own use): a token whose
 // K or V row is NaN becomes K = NaN, V = 0, so that it reaches the scores of
-// the queries that see it and no product of the others (0 * NaN).
+// the queries that see it and no product of the others (0 * NaN).  Under a window
+// only the rows that the queries read are brought back, to the front of a buffer
+// with room for those alone; back_lens takes their number.
 template <int D, int ITER>
 __global__ void __launch_bounds__(kKv4Warps * 32)
 kv4_read_kernel(const Kv4Params p) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES, TOK = kv4_tokens<D, ITER>();
+    if (p.back_lens && blockIdx.y == 0) {       // (the grid has a thread to each row of the buffer at least)
+        const int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+        if (b < p.place.B) {
+            const int n = kv4_used(p.place, static_cast<int>(b));
+            p.back_lens[b] = n - kv4_first_row(p.place, n);
+        }
+    }
     const Kv4Unit u = kv4_unit<TOK>(p);
     if (u.left <= 0) return;
     const int lane = lane_id(), sub = lane / LANES, c8 = lane % LANES;
