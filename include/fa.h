@@ -226,12 +226,15 @@ size_t fa_fwd_kvcache_workspace_size(int B, int H, int Nq, int d, int num_splits
  * queries are the last Nq of those positions, and rows past nk_b are never
  * used.  Queries without a key get O = 0, LSE = -inf.  A row whose K or V
  * stands for NaN makes O NaN (and LSE unspecified) for the queries that see
- * it, and reaches no others.  Elements of q are below 2^116 in magnitude (or
- * O of their query is unspecified).
+ * it, and reaches no others.  Elements of q are below 2^116 in magnitude, and
+ * those of V below 2^100 (or O of their queries is unspecified).
  *   Values may differ in size as they like, whether a mask hides them or not: in a
  * sum p v each p times a row's scale is held to 2^-11 of itself or to 2^-21 of the
  * largest of its query, whichever is more (few rows; chunks: p to 2^-8).  Terms with
- * p below 2^-126 of a query's largest are 0.
+ * p below 2^-126 of a query's largest are 0.  With few rows a product in a score is
+ * cut at 2^-13 of the query's largest |q| times the row's scale: no more than fp32
+ * rounding where a query's elements lie within about 2^6 of each other, up to d
+ * 2^-13 scale s max |q| where one channel stands far above all others.
  *   Few query rows to a key/value head (Nq * H / Hkv up to about 100, more where
  * the whole problem is small) run on kernels that multiply the 4-bit codes as
  * they are; more are run by reading the rows in use back into the workspace for

@@ -32,7 +32,11 @@
 // next to z.  (The products are exact, but the tensor core takes an fp16 subnormal for
 // a number of 2^-14 when it lines products up to add them, and cuts what lies 2^-23
 // below the largest: up to 2^-13 of the largest w of 16 keys, in units of a code.  z is
-// cut as c is.)  Everything else is fp32, the row sums take the unrounded p.
+// cut as c is.  In the scores, sums of q c, it is 2^-13 of the largest |q| of 16
+// channels: nothing for q's eight bits while its elements are within 2^6 of each
+// other.  Codes at a byte's high half everywhere would make both 2^-17, for 2 more
+// shifts to 8 codes, a tenth of a tile's instructions.)  Everything else is fp32, the
+// row sums take the unrounded p.
 //
 // What bounds it: with R = Nq * H / Hkv query rows to a key/value head the
 // cache is D + 4 bytes a token and head for 4 R D operations, so up to a dozen

@@ -246,3 +246,28 @@ def test_a_nan_query_without_a_key(bad, Nq, H, Hkv, d, num_splits):
     assert torch.isnan(o[0, Nq - 1, 0]).all()
     o[0, Nq - 1, 0] = clean[0, Nq - 1, 0]
     assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("channel", [0, 1, 37])
+@pytest.mark.parametrize("large", [8.0, 64.0, 512.0])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_queries_with_one_large_channel(d, channel, large, num_splits):
+    # K has its zero in that channel, so that the others make the scores.  A
+    # product q c is cut at 2^-13 of the largest |q| of its 16 channels, 18 numbers
+    # to a step and d / 16 steps: x is off by 18 2^-13 (d / 16) scale s max |q|
+    # beyond the rounding that grows with the sums themselves; where q's elements
+    # lie within 2^6 of each other nothing is cut (8 bits of q and 4 of c on a grid
+    # of 2^-23 below 2^-14 of the largest), which small parts of q make 2^-20 here.
+    n = 1024
+    cache = random_cache(1, n, 1, d, 5)
+    q = queries(1, 1, 8, d, 7)
+    q[..., channel] = q[..., channel].sign() * large
+    codes, z = cache["k_codes"][..., channel // 2], (cache["k_words"] & 15).to(torch.uint8)
+    codes.copy_((codes & 0x0f) | (z << 4) if channel % 2 else (codes & 0xf0) | z)
+    x = d ** -0.5 * (q[0, 0].double() @ stands_for(cache["k_codes"], cache["k_words"])[0, 0].T)
+    _, lse = fa.forward_kv4(q, cache, causal=True, num_splits=num_splits)
+    top = (d ** -0.5 * scales(cache["k_words"])).max()
+    A = top * 30 * q[0, 0].double().abs().sum(-1)
+    bound = 18 * 2.0 ** -13 * (d / 16) * top * large + (d + 8) * 2.0 ** -24 * A + 2.0 ** -19
+    assert ((lse[0, :, 0].double() - torch.logsumexp(x, -1)).abs() <= bound).all()
