@@ -271,3 +271,37 @@ def test_queries_with_one_large_channel(d, channel, large, num_splits):
     A = top * 30 * q[0, 0].double().abs().sum(-1)
     bound = 18 * 2.0 ** -13 * (d / 16) * top * large + (d + 8) * 2.0 ** -24 * A + 2.0 ** -19
     assert ((lse[0, :, 0].double() - torch.logsumexp(x, -1)).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("spread", [4, 11, 40, 110])
+@pytest.mark.parametrize("seed", range(12))
+def test_random_scales(spread, seed):
+    # every row's values another power of two, rows of zeros among them, NaN rows
+    # where no query looks; heads, queries, lengths, masks and splits by the seed
+    g = torch.Generator("cpu").manual_seed(1000 * spread + seed)
+    pick = lambda *of: of[int(torch.randint(0, len(of), (1,), generator=g))]  # noqa: E731
+    B, Hkv, G, Nq, d = pick(1, 3, 7), pick(1, 2), pick(1, 2, 3, 7), pick(1, 1, 2, 5), pick(64, 128)
+    Nk = pick(8, 72, 520, 1800)
+    causal, window = pick((False, 0), (True, 0), (True, 3), (True, 70), (True, 500))
+    lens = torch.randint(0, Nk + 1, (B,), generator=g).to(torch.int32)
+    cache = random_cache(B, Nk, Hkv, d, seed)
+    up = torch.randint(-(spread // 2), spread // 2 + 1, (B, Hkv, Nk), generator=g)
+    cache["v_words"] += (up << 7).to(torch.int16).to(DEV)
+    cache["v_words"][torch.rand((B, Hkv, Nk), generator=g).to(DEV) < 0.05] = 0
+    for b, n in enumerate(lens.tolist()):
+        first = max(0, n - Nq - window + 1) if window else 0
+        for name in ("k_words", "v_words"):
+            cache[name][b, :, n:] = 0x7fc0
+            cache[name][b, :, :first] = 0x7fc0
+    clean = {n: t.clone() for n, t in cache.items()}
+    for name in ("k_words", "v_words"):
+        clean[name][clean[name] == 0x7fc0] = 0          # (0 * NaN in the reference's product)
+    q = queries(B, Nq, G * Hkv, d, seed)
+    num_splits = pick(0, 1, 3)
+    O, L, bo = tight_reference(q, clean, lens.tolist(), causal, window, d ** -0.5)
+    # (35 query rows to a key/value head at most: on the codes)
+    o, lse = fa.forward_kv4(q, cache, lens.to(DEV), causal=causal, window=window, num_splits=num_splits)
+    assert fa.fa_get_device_error() == 0
+    err = (o.double() - O).abs()
+    assert torch.isfinite(o).all() and (err <= bo).all(), "O: %.3g of its bound" % (err / bo.clamp(min=1e-300)).max()
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(L))
