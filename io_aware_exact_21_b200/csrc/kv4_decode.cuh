@@ -34,9 +34,10 @@
 // below the largest: up to 2^-13 of the largest w of 16 keys, in units of a code.  z is
 // cut as c is.  In the scores, sums of q c, it is 2^-13 of the largest |q| of 16
 // channels: nothing for q's eight bits while its elements are within 2^6 of each
-// other.  Codes at a byte's high half everywhere would make both 2^-17, for 2 more
-// shifts to 8 codes, a tenth of a tile's instructions.)  Everything else is fp32, the
-// row sums take the unrounded p.
+// other, 1e-3 of the LSE where one is 100 times the rest.  All codes at a byte's high
+// half would make both 2^-17, for 2 more shifts to 8 codes: 44.9 us for 42.9 with
+// the scores' alone at B 16, 47.6 with both.)  Everything else is fp32, the row sums
+// take the unrounded p.
 //
 // What bounds it: with R = Nq * H / Hkv query rows to a key/value head the
 // cache is D + 4 bytes a token and head for 4 R D operations, so up to a dozen
@@ -52,8 +53,8 @@
 // kv4_merge_kernel).
 //
 // Measured on one B200 at 16 requests x 16 heads, one query each, caches of
-// 4096 to 8192 rows, d = 128 (208 MB, 31.7 us at the measured copy rate): 43 us
-// with the merge, which is 3 of them.  The same with the arithmetic left out 34
+// 4096 to 8192 rows, d = 128 (208 MB, 31.7 us at the measured copy rate): 43 to 45
+// us on different boards with the merge, which is 3 of them.  The same with the arithmetic left out 34
 // us, with the loads left out 33 us; so both sides matter, and an instruction
 // less a code has been worth more than anything else: 64 us with a tile of 32
 // keys, cp.async and a maximum looked for in each tile; 47 us with equal ranges
